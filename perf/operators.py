@@ -1,0 +1,414 @@
+"""The operators for dense tensors and expert layers, as perf cases: plain forms, and the library's calls.
+
+Three groups of cases:
+  adamw       one AdamW step over many tensors, moments in fp32 or in 8 bits (e4m3 codes with an fp32
+              scale per 256 elements), with or without the global gradient norm that clips it
+  forward/dx  products grouped by expert: Y[t] = W[e(t)] A[t], and its input gradient
+  dw          the weight gradient of every expert, dW[e] = sum over its tokens of dY[t] A[t]^T
+"""
+import random
+
+import numpy as np
+import torch
+
+own = False
+
+DEV = "cuda"
+BLOCK = 256                       # elements that share one scale of the 8-bit moments
+LR, BETA1, BETA2, EPS, WD, MAX_NORM = 1e-4, 0.9, 0.95, 1e-8, 0.1, 1.0
+STEPS_BEFORE, T_MAX = 100, 2000
+SCALE_FLOOR = 2.0 ** -100         # smallest scale of a block
+LAYER = (4096 * 4096,) * 4 + (11008 * 4096,) * 3
+
+
+def listed():
+    return [
+        # the 65 norm gains of a 32-layer stack of width 4,096: a step that is all latency
+        dict(name="adamw_norms", kind="adamw", sizes="gains", state="f32", param="f32", grad="f32", live=False, clip=False),
+        # the seven projections of a 7B-shaped layer: fp32 master weights, bf16 gradients and live copy
+        dict(name="adamw_layer_f32", kind="adamw", sizes="layer", state="f32", param="f32", grad="bf16", live=True, clip=False),
+        # the same layer with 8-bit moments and the clipped gradient norm, as when memory is short
+        dict(name="adamw_layer_8bit", kind="adamw", sizes="layer", state="e4m3", param="f32", grad="bf16", live=True, clip=True),
+        # adapters, biases and odd-sized tensors trained in bf16 with 8-bit moments
+        dict(name="adamw_ragged_8bit", kind="adamw", sizes="ragged", count=120, total=6_000_000, state="e4m3", param="bf16", grad="bf16", live=False, clip=True),
+        # one token sent to two of eight experts: a decode step of a single sequence
+        dict(name="forward_token", kind="forward", E=8, T=2, R=4096, C=4096, type="bf16", skew=0, spare=0),
+        # a decode step of a batch: every expert has a few tokens, the weights are the traffic
+        dict(name="forward_decode", kind="forward", E=8, T=96, R=11008, C=4096, type="bf16", skew=1, spare=0),
+        # a training batch through the up projection of eight experts
+        dict(name="forward_batch", kind="forward", E=8, T=8192, R=11008, C=4096, type="bf16", skew=1, spare=0),
+        # many small fp16 experts, odd widths, some without a token, rows behind the last expert
+        dict(name="forward_ragged", kind="forward", E=48, T=5000, R=1416, C=2056, type="f16", skew=3, spare=77),
+        # the input gradient of that training batch
+        dict(name="dx_batch", kind="dx", E=8, T=8192, R=11008, C=4096, type="bf16", skew=1, spare=0),
+        # the input gradient of a short ragged batch
+        dict(name="dx_ragged", kind="dx", E=16, T=777, R=2056, C=1416, type="f16", skew=2, spare=5),
+        # the weight gradients of that training batch, fp32
+        dict(name="dw_batch", kind="dw", E=8, T=8192, R=11008, C=4096, type="bf16", out="f32", add=False, skew=1, spare=0),
+        # many small experts, the second micro-batch added to the first one's gradient
+        dict(name="dw_ragged", kind="dw", E=48, T=5000, R=1416, C=2056, type="bf16", out="f32", add=True, skew=3, spare=77),
+    ]
+
+
+def _log(rng, lo, hi):
+    return min(hi, max(lo, int(round(lo * (hi / lo) ** rng.random()))))
+
+
+def draw(rng):
+    kind = rng.choice(("adamw", "forward", "dx", "dw"))
+    if kind == "adamw":
+        total = _log(rng, 3000, 150_000_000)
+        return dict(kind=kind, sizes="ragged", count=_log(rng, 1, 200), total=total, state=rng.choice(("f32", "e4m3")),
+                    param=rng.choice(("f32", "bf16")), grad=rng.choice(("f32", "bf16", "f16")), live=rng.random() < 0.5,
+                    clip=rng.random() < 0.5, pick=rng.randrange(1 << 20))
+    while True:
+        E, T = _log(rng, 1, 64), _log(rng, 1, 8192)
+        R, C = 8 * _log(rng, 8, 1376), 8 * _log(rng, 8, 1376)
+        if E * R * C <= 8 * 11008 * 4096 and T * R * C <= 8192 * 11008 * 4096:
+            break
+    c = dict(kind=kind, E=E, T=T, R=R, C=C, type=rng.choice(("bf16", "f16")), skew=rng.randrange(4), spare=rng.choice((0, 0, 3, 50)),
+             pick=rng.randrange(1 << 20))
+    if kind == "dw":
+        c["out"] = rng.choice(("f32", "f32", c["type"]))
+        c["add"] = c["out"] == "f32" and rng.random() < 0.5
+    return c
+
+
+# ------------------------------------------------------------------------------------------------
+# sizes: fixed by the case alone, so that work() knows them
+# ------------------------------------------------------------------------------------------------
+
+def _lengths(case):
+    if case["sizes"] == "gains":
+        return [4096] * 65
+    if case["sizes"] == "layer":
+        return list(LAYER)
+    r = random.Random(case.get("pick", 1))
+    shares = [r.expovariate(1.0) + 0.01 for _ in range(case["count"])]
+    return [max(1, int(case["total"] * s / sum(shares))) for s in shares]
+
+
+def _counts(case):
+    """Tokens of every expert, in no particular order: skew 0 spreads them evenly, more skew less so."""
+    E, T, skew = case["E"], case["T"], case["skew"]
+    r = random.Random(case.get("pick", 1))
+    shares = [1.0 if skew == 0 else r.expovariate(1.0) ** (0.5 * skew) for _ in range(E)]
+    if skew >= 2 and E > 2:
+        shares[r.randrange(E)] = 0.0
+    edges = np.floor(np.cumsum([0.0] + shares) / sum(shares) * T + 0.5).astype(np.int64)
+    edges[-1] = T
+    return np.diff(edges)
+
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+SZ = {"f32": 4, "bf16": 2, "f16": 2, "e4m3": 1}
+
+
+# ------------------------------------------------------------------------------------------------
+# inputs
+# ------------------------------------------------------------------------------------------------
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _pieces(flat, lengths, starts):
+    return [flat[s:s + n] for n, s in zip(lengths, starts)]
+
+
+def _prepare_adamw(case, seed):
+    g = _gen(seed)
+    lengths = _lengths(case)
+    room = [-(-n // BLOCK) * BLOCK for n in lengths]
+    starts = np.concatenate([[0], np.cumsum(room)])
+    N = int(starts[-1])
+    # one buffer for each kind of value, every tensor at a block's start, zeros between tensors
+    held = torch.zeros(N, dtype=torch.bool, device=DEV)
+    decay = torch.zeros(N // BLOCK, device=DEV)
+    for i, (n, s) in enumerate(zip(lengths, starts)):
+        held[int(s):int(s) + n] = True
+        decay[int(s) // BLOCK:int(starts[i + 1]) // BLOCK] = 0.0 if n <= 4096 else 1.0      # gains and biases do not decay
+
+    def normal(std):
+        return torch.randn(N, generator=g, device=DEV).mul_(std).mul_(held)
+
+    s = {"case": case, "decay": decay, "lengths": lengths, "starts": [int(x) for x in starts[:-1]]}
+    s["p"] = normal(0.02).to(DT[case["param"]])
+    s["g"] = normal(1e-3).to(DT[case["grad"]])
+    m, r = normal(3e-4), normal(1e-3).abs_()
+    if case["state"] == "f32":
+        s["m"], s["v"] = m, r.square_()
+    else:
+        for name, x in (("m", m), ("v", r)):
+            x = x.view(-1, BLOCK)
+            sc = (x.abs().amax(1) / 448).clamp_(min=SCALE_FLOOR)
+            s[name] = (x / sc[:, None]).clamp_(-448, 448).to(torch.float8_e4m3fn).view(-1)
+            s[name + "_scale"] = sc
+    s["live"] = s["p"].to(torch.bfloat16) if case["live"] else None
+    s["step"] = torch.tensor([STEPS_BEFORE, 0], dtype=torch.int32, device=DEV)
+    b1, b2 = float(np.float32(BETA1)), float(np.float32(BETA2))
+    t = np.arange(T_MAX + 1, dtype=np.float64)
+    t[0] = np.inf
+    s["bc1"] = torch.from_numpy(np.float32(1 / (1 - b1 ** t))).to(DEV)
+    s["bc2"] = torch.from_numpy(np.float32(1 / (1 - b2 ** t))).to(DEV)
+    s["norm"] = torch.zeros(2, device=DEV)
+    if own:
+        _plan_adamw(s)
+    return s
+
+
+def _prepare_grouped(case, seed):
+    g = _gen(seed)
+    E, T, R, C, dt = case["E"], case["T"], case["R"], case["C"], DT[case["type"]]
+    counts = np.roll(_counts(case), seed % E)
+    rows = T + case["spare"]
+
+    def normal(shape, std):
+        return torch.randn(shape, generator=g, device=DEV, dtype=dt).mul_(std)
+
+    s = {"case": case, "longest": int(counts.max())}
+    s["offsets"] = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).to(DEV)
+    if case["kind"] != "dx":
+        s["A"] = normal((rows, C), 1.0)
+    else:
+        s["A"] = torch.zeros((rows, C), dtype=dt, device=DEV)
+    if case["kind"] != "dw":
+        s["W"] = normal((E, R, C), 0.02)
+    elif case["add"]:
+        s["W"] = torch.randn((E, R, C), generator=g, device=DEV)
+    else:
+        s["W"] = torch.zeros((E, R, C), dtype=DT[case["out"]], device=DEV)
+    if case["kind"] != "forward":
+        s["Y"] = normal((rows, R), 1.0)
+    else:
+        s["Y"] = torch.zeros((rows, R), dtype=dt, device=DEV)
+    if own:
+        _plan_grouped(s)
+    return s
+
+
+def prepare(case, seed):
+    return _prepare_adamw(case, seed) if case["kind"] == "adamw" else _prepare_grouped(case, seed)
+
+
+# ------------------------------------------------------------------------------------------------
+# the library's calls
+# ------------------------------------------------------------------------------------------------
+
+def _plan_adamw(s):
+    """The tensor list and hyper-parameters that a program keeps from step to step."""
+    from masked_optimizer_step_b200 import binding as sf
+    case = s["case"]
+    out = []
+    for n, a in zip(s["lengths"], s["starts"]):
+        b, e = a // BLOCK, -(-(a + n) // BLOCK)
+        scales = {} if case["state"] == "f32" else dict(m_scale=s["m_scale"][b:e], v_scale=s["v_scale"][b:e])
+        out.append(sf.dense_tensor(s["p"][a:a + n], s["g"][a:a + n], s["m"][a:a + n], s["v"][a:a + n],
+                                   live=None if s["live"] is None else s["live"][a:a + n],
+                                   decay=0.0 if n <= 4096 else 1.0, **scales))
+    s["tensors"] = sf.DenseTensors(out)
+    s["hp"] = sf.AdamParams(lr=LR, beta1=BETA1, beta2=BETA2, eps=EPS, wd=WD, t_max=T_MAX, device=DEV)
+    s["status"] = sf.status_word(DEV)
+    s["ws"] = sf.grad_norm_workspace(s["tensors"], DEV) if case["clip"] else None
+    s["sf"] = sf
+
+
+def _plan_grouped(s):
+    from masked_optimizer_step_b200 import binding as sf
+    s["problem"] = sf.grouped_problem(s["A"], s["W"], s["Y"], s["offsets"])
+    s["status"] = sf.status_word(DEV)
+    s["sf"] = sf
+
+
+def _own_adamw(s):
+    sf, clip = s["sf"], s["case"]["clip"]
+    if clip:
+        sf.sf_grad_norm(s["tensors"], s["norm"], s["ws"], max_norm=MAX_NORM, status=s["status"])
+    sf.sf_adamw_step(s["tensors"], s["hp"], s["step"], factor=s["norm"] if clip else None, status=s["status"])
+
+
+def _own_grouped(s):
+    sf, case = s["sf"], s["case"]
+    if case["kind"] == "forward":
+        sf.sf_grouped_forward(s["problem"], s["status"])
+    elif case["kind"] == "dx":
+        sf.sf_grouped_dx(s["problem"], s["status"])
+    else:
+        sf.sf_grouped_dw(s["problem"], s["status"], accumulate=case["add"])
+
+
+# ------------------------------------------------------------------------------------------------
+# the plain forms
+# ------------------------------------------------------------------------------------------------
+
+def _encode(x, positive):
+    """fp32 values in blocks -> (codes, scale): scale = largest magnitude / 448, codes e4m3."""
+    sc = (x.abs().amax(1) * float(np.float32(1 / 448))).clamp(min=SCALE_FLOOR)
+    y = (x * (1.0 / sc)[:, None]).clamp(-448, 448)
+    if positive:                       # a positive value keeps a positive code
+        y = torch.where(x > 0, y.clamp(min=2.0 ** -9), y)
+    return y.to(torch.float8_e4m3fn).view(-1), sc
+
+
+def _plain_adamw(s):
+    case = s["case"]
+    f32 = lambda v: float(np.float32(v))  # noqa: E731
+    g = s["g"].float()
+    if case["clip"]:
+        norm = s["g"].double().square().sum().sqrt()
+        s["norm"][0] = norm
+        s["norm"][1] = (MAX_NORM / (norm + 1e-6)).clamp(max=1.0)
+        g = g * s["norm"][1]
+    s["step"][0] += 1
+    t = s["step"][0].long()
+    bc1, root2 = s["bc1"][t], s["bc2"][t].sqrt()
+    if case["state"] == "f32":
+        m, v = s["m"], s["v"]
+    else:
+        m = (s["m"].float().view(-1, BLOCK) * s["m_scale"][:, None]).view(-1)
+        r = (s["v"].float().view(-1, BLOCK) * s["v_scale"][:, None]).view(-1)
+        v = r * r
+    m = m * f32(BETA1) + g * f32(np.float32(1) - np.float32(BETA1))
+    v = v * f32(BETA2) + g * g * f32(np.float32(1) - np.float32(BETA2))
+    r = v.sqrt()
+    u = m * bc1 / (r * root2 + f32(EPS))
+    p = s["p"].float()
+    wd = (s["decay"] * f32(np.float32(LR) * np.float32(WD))).repeat_interleave(BLOCK)
+    p = p - u * f32(LR) - p * wd
+    s["p"].copy_(p)
+    if s["live"] is not None:
+        s["live"].copy_(p)
+    if case["state"] == "f32":
+        s["m"].copy_(m)
+        s["v"].copy_(v)
+    else:
+        for name, x, pos in (("m", m, False), ("v", r, True)):
+            code, sc = _encode(x.view(-1, BLOCK), pos)
+            s[name].copy_(code)
+            s[name + "_scale"].copy_(sc)
+
+
+def _padded(s, x):
+    """Rows of x by expert, [E, longest, width] in fp32, zeros behind an expert's last row; their indexes."""
+    off = s["offsets"].long()
+    at = off[:-1, None] + torch.arange(s["longest"], device=DEV)
+    inside = at < off[1:, None]
+    at = torch.where(inside, at, 0)
+    return torch.where(inside[:, :, None], x[at].float(), 0.0), at[inside], inside
+
+
+def _plain_grouped(s):
+    case = s["case"]
+    if s["longest"] == 0:
+        return
+    if case["kind"] == "dw":
+        a, _, _ = _padded(s, s["A"])
+        y, _, _ = _padded(s, s["Y"])
+        w = torch.bmm(y.transpose(1, 2), a)
+        s["W"].copy_(s["W"] + w if case["add"] else w)
+        return
+    src, dst = ("A", "Y") if case["kind"] == "forward" else ("Y", "A")
+    x, at, inside = _padded(s, s[src])
+    w = s["W"].float()
+    out = torch.bmm(x, w.transpose(1, 2) if case["kind"] == "forward" else w)
+    s[dst][at] = out[inside].to(s[dst].dtype)
+
+
+def run(state):
+    case = state["case"]
+    if case["kind"] == "adamw":
+        (_own_adamw if own else _plain_adamw)(state)
+        out = {k: state[k] for k in ("p", "m", "v", "step")}
+        if case["state"] != "f32":
+            out.update(m_scale=state["m_scale"], v_scale=state["v_scale"])
+        if state["live"] is not None:
+            out["live"] = state["live"]
+        if case["clip"]:
+            out["norm"] = state["norm"]
+        return out
+    (_own_grouped if own else _plain_grouped)(state)
+    return {"forward": state["Y"], "dx": state["A"], "dw": state["W"]}[case["kind"]]
+
+
+# ------------------------------------------------------------------------------------------------
+# work, and the operators in 64 bits
+# ------------------------------------------------------------------------------------------------
+
+def work(case):
+    if case["kind"] == "adamw":
+        n = sum(_lengths(case))
+        blocks = sum(-(-k // BLOCK) for k in _lengths(case))
+        per = 2 * SZ[case["param"]] + SZ[case["grad"]] + 4 * SZ[case["state"]] + (2 if case["live"] else 0)
+        extra = 16 * blocks if case["state"] != "f32" else 0
+        return {"bytes": per * n + extra, "flops": 20 * n}
+    counts = _counts(case)
+    T, R, C = case["T"], case["R"], case["C"]
+    busy = int((counts > 0).sum())
+    rows = 2 * T * (R + C)
+    if case["kind"] == "dw":
+        return {"bytes": rows + case["E"] * R * C * SZ[case["out"]] * (2 if case["add"] else 1), "flops": 2 * T * R * C}
+    return {"bytes": rows + 2 * busy * R * C, "flops": 2 * T * R * C}
+
+
+def _exact_adamw(s):
+    case = s["case"]
+    d = torch.float64
+    g = s["g"].to(d)
+    out = {}
+    if case["clip"]:
+        norm = (g * g).sum() ** 0.5
+        factor = min(1.0, MAX_NORM / (float(norm) + 1e-6))
+        out["norm"] = torch.tensor([float(norm), factor], dtype=d)
+        g = g * factor
+    t = STEPS_BEFORE + 1
+    b1, b2 = float(np.float32(BETA1)), float(np.float32(BETA2))
+    m, v = s["m"].to(torch.float32).to(d), s["v"].to(torch.float32).to(d)
+    if case["state"] != "f32":
+        m = m * s["m_scale"].to(d).repeat_interleave(BLOCK)
+        v = (v * s["v_scale"].to(d).repeat_interleave(BLOCK)) ** 2
+    m = b1 * m + (1 - b1) * g
+    v = b2 * v + (1 - b2) * g ** 2
+    step = (m / (1 - b1 ** t)) / ((v / (1 - b2 ** t)) ** 0.5 + EPS)
+    p = s["p"].to(d)
+    p = p - LR * step - LR * WD * s["decay"].to(d).repeat_interleave(BLOCK) * p
+    out["p"] = p
+    out["step"] = None
+    if s["live"] is not None:
+        out["live"] = p
+    if case["state"] == "f32":
+        out["m"], out["v"] = m, v
+    else:
+        for name, x in (("m", m), ("v", v ** 0.5)):
+            scale = x.view(-1, BLOCK).abs().max(dim=1).values / 448
+            scale = torch.where(scale < SCALE_FLOOR, torch.full_like(scale, SCALE_FLOOR), scale)
+            y = x / scale.repeat_interleave(BLOCK)
+            # nearest e4m3 value: eight steps to each power of two, 2^-9 apart below 2^-6, ties to even
+            grain = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)
+            y = torch.round(y / grain) * grain
+            if name == "v":
+                y = torch.where((x > 0) & (y == 0), torch.full_like(y, 2.0 ** -9), y)
+            out[name], out[name + "_scale"] = y, scale
+    return out
+
+
+def _exact_grouped(s):
+    case = s["case"]
+    d = torch.float64
+    edges = s["offsets"].tolist()
+    spans = list(zip(range(case["E"]), edges[:-1], edges[1:]))
+    if case["kind"] == "dw":
+        out = s["W"].to(d) if case["add"] else torch.zeros(s["W"].shape, dtype=d, device=DEV)
+        for e, a, b in spans:
+            out[e] += s["Y"][a:b].to(d).t() @ s["A"][a:b].to(d)
+        return out
+    src, dst = ("A", "Y") if case["kind"] == "forward" else ("Y", "A")
+    out = s[dst].to(d)
+    for e, a, b in spans:
+        w = s["W"][e].to(d)
+        out[a:b] = s[src][a:b].to(d) @ (w.t() if case["kind"] == "forward" else w)
+    return out
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    return _exact_adamw(s) if case["kind"] == "adamw" else _exact_grouped(s)
