@@ -51,6 +51,7 @@ extern "C" {
 #define SF_STATUS_NONFINITE      0x2u  /* a non-finite gradient, moment or weight was produced */
 #define SF_STATUS_BAD_TOKEN      0x4u  /* a token or row id outside [0, R) was ignored */
 #define SF_STATUS_WAIT_TIMEOUT   0x8u  /* a kernel gave up a bounded wait and skipped its work */
+#define SF_STATUS_BAD_OFFSET     0x10u /* expert offsets fall or leave [0, T]: nothing was computed */
 /* Test hook: with SF_TEST_DW_WITHHOLD=1 in the environment, sf_masked_dw's first launch withholds
  * one pipeline stage of CTA 0, so that a bounded wait runs out and WAIT_TIMEOUT is raised. */
 
@@ -368,6 +369,77 @@ int sf_mask_update_phase(const sf_mask *masks /* host [n_masks] */,
                          int phase, uint32_t *dev_status, sf_stream stream);
 int sf_masked_dw_phase(const sf_dw_problem *probs /* host [n] */, int n, void *ws, size_t ws_bytes,
                        int phase, uint32_t *dev_status, sf_stream stream);
+
+/* ---- element types of the dense-tensor and expert-grouped calls ------------------------------ */
+#define SF_TYPE_F32  0
+#define SF_TYPE_BF16 1
+#define SF_TYPE_F16  2
+#define SF_TYPE_E4M3 3   /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448 */
+
+/* ---- sf_grad_norm / sf_adamw_step: dense tensors ----------------------------------------------
+ * No counterpart in the paper: the tensors a model has beside its int8 matrices (norm gains,
+ * biases, heads, adapters, experts' weights) take a dense AdamW step. A call takes any number of
+ * tensors of any lengths at once.
+ * Per element, with f = factor[1] (1 when factor is NULL), t = step[0] + 1 and every operation
+ * rounded in fp32:
+ *   g  = clamp(grad * f, -clip, clip)                   (clip <= 0: no clamp)
+ *   m1 = beta1 * m + one_minus_b1 * g,   v1 = beta2 * v + one_minus_b2 * g * g
+ *   u  = (m1 * bc1[t]) / (sqrt(v1) * sqrt(bc2[t]) + eps)
+ *   p  = p - lr * u - (decay * lr * wd) * p             (p held in fp32, rounded once when bf16)
+ * and live = bf16(p) where live is given. bc1/bc2 are sf_adam_tables' (a step count above t_max
+ * uses entry t_max).
+ * Moments are fp32 (SF_TYPE_F32: m and v), or 8 bits (SF_TYPE_E4M3): e4m3 codes with one fp32
+ * scale per 256 consecutive elements (SF_DENSE_BLOCK; the last block may be short), holding
+ *   m = code_m * m_scale       and       sqrt(v) = code_v * v_scale.
+ * After the step a block's scale is (largest magnitude in the block) / 448, at least 2^-100, and a
+ * code is the nearest e4m3 value to the moment / scale, ties to even; a positive sqrt(v) never
+ * rounds to a zero code. The square root halves v's range in powers of two, so that codes cover a
+ * ratio of 2^35 in v; the fp32 scale follows the block's largest value exactly, so that a decay of
+ * the whole block is never lost to rounding.
+ * step [2] device int32: [0] the steps taken so far, raised by one by a call that steps (all
+ * tensors of a call share it); [1] must be 0 and is 0 again when the call has run. Two calls that
+ * can overlap need step words of their own.
+ * factor: the two floats of sf_grad_norm, or NULL. When factor[1] is 0 or NaN (the gradient was not
+ * finite) the step is skipped: every tensor and the step count stay as they are, and
+ * SF_STATUS_NONFINITE is set. A step that produces a non-finite weight or moment sets it too.
+ *
+ * sf_grad_norm: out[0] = inv_scale * sqrt(sum of squares of every gradient of every tensor) (squares
+ * in fp32, sums in fp64, in a fixed order), out[1] = inv_scale * min(1, max_norm / (out[0] + 1e-6)),
+ * or inv_scale when max_norm <= 0; out[1] = 0 (and SF_STATUS_NONFINITE) when the norm is not finite.
+ * inv_scale undoes a loss scale (1 for none). Only n, g and g_type of a tensor are read. ws:
+ * sf_grad_norm_ws_bytes() bytes, 16-byte aligned, zeroed once by the caller; every call leaves it
+ * ready for the next. Calls that can overlap need workspaces of their own.
+ *
+ * Requirements: n >= 0; p, g, m, v, live 16-byte aligned; p fp32 or bf16; g fp32, bf16 or fp16;
+ * m_scale, v_scale present for 8-bit moments. Buffers of one call must not overlap.
+ * Launches: one per 384 non-empty tensors. Errors: SF_ERR_ARG, SF_ERR_ALIGN.
+ */
+#define SF_DENSE_BLOCK 256
+#define SF_DENSE_PER_LAUNCH 384
+
+typedef struct sf_dense {
+    int64_t     n;           /* elements */
+    void       *p;           /* weights, p_type */
+    const void *g;           /* gradient, g_type */
+    void       *m;           /* first moment, state_type */
+    void       *v;           /* second moment (8-bit: codes of its root), state_type */
+    float      *m_scale;     /* [ceil(n / 256)], 8-bit moments only */
+    float      *v_scale;
+    uint16_t   *live;        /* bf16 bits, may be NULL */
+    float       decay;       /* multiplies hp->wd for this tensor */
+    int32_t     p_type;
+    int32_t     g_type;
+    int32_t     state_type;
+} sf_dense;
+
+size_t sf_grad_norm_ws_bytes(const sf_dense *t /* host [n] */, int n);
+
+int sf_grad_norm(const sf_dense *t /* host [n] */, int n, float inv_scale, float max_norm,
+                 float *out /* device [2] */, void *ws, size_t ws_bytes, uint32_t *dev_status,
+                 sf_stream stream);
+
+int sf_adamw_step(const sf_dense *t /* host [n] */, int n, const sf_adam *hp, int32_t *step,
+                  const float *factor, uint32_t *dev_status, sf_stream stream);
 
 /* ---- helpers (not on the hot path) ------------------------------------------------------ */
 

@@ -22,6 +22,7 @@ SF_STATUS_SLOT_OVERFLOW = 0x1
 SF_STATUS_NONFINITE = 0x2
 SF_STATUS_BAD_TOKEN = 0x4
 SF_STATUS_WAIT_TIMEOUT = 0x8
+SF_STATUS_BAD_OFFSET = 0x10
 
 SF_SRC_TOKENS = 0
 SF_SRC_OUTPUT_BF16 = 1
@@ -31,6 +32,13 @@ SF_SRC_WORDS = 3
 SF_PHASE_ALL = 0
 SF_PHASE_FIRST = 1
 SF_PHASE_SECOND = 2
+
+SF_TYPE_F32 = 0
+SF_TYPE_BF16 = 1
+SF_TYPE_F16 = 2
+SF_TYPE_E4M3 = 3
+SF_DENSE_BLOCK = 256
+SF_DENSE_PER_LAUNCH = 384
 
 SF_DW_MAX_PER_LAUNCH = 96
 SF_MASKS_PER_LAUNCH = 240
@@ -80,6 +88,11 @@ class sf_adam(ctypes.Structure):
                 ("t_max", _I32)]
 
 
+class sf_dense(ctypes.Structure):
+    _fields_ = [("n", _I64), ("p", _P), ("g", _P), ("m", _P), ("v", _P), ("m_scale", _P), ("v_scale", _P),
+                ("live", _P), ("decay", _F), ("p_type", _I32), ("g_type", _I32), ("state_type", _I32)]
+
+
 _lib = None
 
 
@@ -121,6 +134,12 @@ def load():
     L.sf_quantize_init.argtypes = [_P, ctypes.c_int, ctypes.c_int, _P, _P, _P, _P, _P]
     for name in ("sf_checkpoint_save", "sf_checkpoint_restore"):
         getattr(L, name).argtypes = [ctypes.POINTER(sf_matrix), ctypes.POINTER(sf_checkpoint), ctypes.c_int, _P, _P]
+        getattr(L, name).restype = ctypes.c_int
+    L.sf_grad_norm_ws_bytes.restype = ctypes.c_size_t
+    L.sf_grad_norm_ws_bytes.argtypes = [ctypes.POINTER(sf_dense), ctypes.c_int]
+    L.sf_grad_norm.argtypes = [ctypes.POINTER(sf_dense), ctypes.c_int, _F, _F, _P, _P, ctypes.c_size_t, _P, _P]
+    L.sf_adamw_step.argtypes = [ctypes.POINTER(sf_dense), ctypes.c_int, ctypes.POINTER(sf_adam), _P, _P, _P, _P]
+    for name in ("sf_grad_norm", "sf_adamw_step"):
         getattr(L, name).restype = ctypes.c_int
     for name in ("sf_mask_init", "sf_mask_update", "sf_masked_dw", "sf_embed_grad", "sf_adam_tables",
                  "sf_sparse_update", "sf_quantize_init", "sf_mask_update_phase", "sf_masked_dw_phase",
@@ -412,3 +431,130 @@ def sf_checkpoint_save(mats, ckpts, status=None, stream=None):
 
 def sf_checkpoint_restore(mats, ckpts, status=None, stream=None):
     _ckpt_call("sf_checkpoint_restore", mats, ckpts, status, stream)
+
+
+# ---------------------------------------------------------------------------------------------
+# Dense tensors: AdamW and the global gradient norm
+# ---------------------------------------------------------------------------------------------
+
+_TYPE_OF = {torch.float32: SF_TYPE_F32, torch.bfloat16: SF_TYPE_BF16, torch.float16: SF_TYPE_F16,
+            torch.float8_e4m3fn: SF_TYPE_E4M3, torch.uint8: SF_TYPE_E4M3}
+
+
+def _type(t, allowed, what) -> int:
+    k = _TYPE_OF.get(t.dtype)
+    if k not in allowed:
+        raise ValueError(f"{what}: {t.dtype} is not supported")
+    return k
+
+
+def _one_device(*tensors):
+    """The index of the device that all the given tensors (None among them) are on."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1 or next(iter(devs)).type != "cuda":
+        raise ValueError("device tensors on one GPU expected")
+    return next(iter(devs)).index
+
+
+def _on_current(index: int):
+    if torch.cuda.current_device() != index:
+        raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
+
+
+def dense_tensor(p, g, m, v, live=None, decay: float = 1.0, m_scale=None, v_scale=None) -> Desc:
+    """One tensor of an AdamW step. p fp32 or bf16; g fp32, bf16 or fp16; m, v fp32, or e4m3 codes
+    (float8_e4m3fn or uint8) with one fp32 scale per SF_DENSE_BLOCK elements; live (optional) bf16,
+    written with the stepped weights; decay multiplies the step's weight decay (0: none). All
+    contiguous, of one length."""
+    n = p.numel()
+    for t in (p, g, m, v, live):
+        if t is not None and (t.numel() != n or not t.is_contiguous()):
+            raise ValueError("p, g, m, v and live must be contiguous and of one length")
+    pt = _type(p, (SF_TYPE_F32, SF_TYPE_BF16), "p")
+    gt = _type(g, (SF_TYPE_F32, SF_TYPE_BF16, SF_TYPE_F16), "g")
+    st = _type(m, (SF_TYPE_F32, SF_TYPE_E4M3), "m")
+    if m.dtype != v.dtype:
+        raise ValueError("m and v must have one type")
+    if live is not None and live.dtype not in (torch.bfloat16, torch.int16):
+        raise ValueError("live must hold bf16")
+    if st == SF_TYPE_E4M3:
+        blocks = -(-n // SF_DENSE_BLOCK)
+        for s in (m_scale, v_scale):
+            if s is None or s.dtype != torch.float32 or s.numel() != blocks or not s.is_contiguous():
+                raise ValueError(f"8-bit moments need {blocks} fp32 scales each")
+    elif m_scale is not None or v_scale is not None:
+        raise ValueError("fp32 moments take no scales")
+    refs = (p, g, m, v, live, m_scale, v_scale)
+    _one_device(*refs)
+    return Desc(sf_dense(n, _ptr(p), _ptr(g), _ptr(m), _ptr(v), _ptr(m_scale), _ptr(v_scale), _ptr(live), decay,
+                         pt, gt, st), *refs)
+
+
+class Dense:
+    """A dense tensor's AdamW state: zero moments (fp32, or 8 bits with their scales) for weights p
+    and gradient g, and optionally a bf16 live copy of p."""
+
+    def __init__(self, p, g, state: int = SF_TYPE_F32, live: bool = False, decay: float = 1.0):
+        if state not in (SF_TYPE_F32, SF_TYPE_E4M3):
+            raise ValueError("moments are SF_TYPE_F32 or SF_TYPE_E4M3")
+        self.p, self.g, self.decay = p, g, decay
+        self.m_scale = self.v_scale = None
+        if state == SF_TYPE_E4M3:
+            blocks = -(-p.numel() // SF_DENSE_BLOCK)
+            self.m_scale = torch.zeros(blocks, dtype=torch.float32, device=p.device)
+            self.v_scale = torch.zeros(blocks, dtype=torch.float32, device=p.device)
+        dt = torch.float32 if state == SF_TYPE_F32 else torch.float8_e4m3fn
+        self.m = torch.zeros(p.shape, dtype=dt, device=p.device)
+        self.v = torch.zeros(p.shape, dtype=dt, device=p.device)
+        self.live = p.to(torch.bfloat16) if live else None
+
+    def desc(self) -> Desc:
+        return dense_tensor(self.p, self.g, self.m, self.v, self.live, self.decay, self.m_scale, self.v_scale)
+
+
+class DenseTensors:
+    """The argument array of a list of dense_tensor() descriptors, built once for many steps."""
+
+    def __init__(self, tensors):
+        self.descs = [t.desc() if isinstance(t, Dense) else t for t in tensors]
+        self.n = len(self.descs)
+        self.arr = (sf_dense * max(self.n, 1))(*[d.c for d in self.descs])
+        refs = [t for d in self.descs for t in d.refs]
+        self.device = _one_device(*refs) if self.n else None
+
+
+def step_words(device=None) -> torch.Tensor:
+    """The device step count of sf_adamw_step: [steps taken, 0]."""
+    return torch.zeros(2, dtype=torch.int32, device=device or "cuda")
+
+
+def grad_norm_workspace(tensors: DenseTensors, device="cuda") -> torch.Tensor:
+    """Zeroed scratch for sf_grad_norm over these tensors."""
+    return torch.zeros(load().sf_grad_norm_ws_bytes(tensors.arr, tensors.n), dtype=torch.uint8, device=device)
+
+
+def _check_words(name, t, dtype, device):
+    if t.dtype != dtype or t.numel() < 2 or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor of two {dtype} expected")
+    if device is not None and t.device.index != device:
+        raise ValueError(f"{name} is on another device than the tensors")
+
+
+def sf_grad_norm(tensors: DenseTensors, out, ws, max_norm: float = 0.0, inv_scale: float = 1.0, status=None,
+                 stream=None):
+    """out (two floats): the gradients' global norm and the factor that clips it, for sf_adamw_step."""
+    _check_words("out", out, torch.float32, tensors.device)
+    _on_current(_one_device(out, ws, status))
+    _check(load().sf_grad_norm(tensors.arr, tensors.n, inv_scale, max_norm, _ptr(out), _ptr(ws),
+                               ws.numel() * ws.element_size(), _ptr(status), _stream(stream)), "sf_grad_norm")
+
+
+def sf_adamw_step(tensors: DenseTensors, hp: AdamParams, step, factor=None, status=None, stream=None):
+    """One AdamW step of every tensor; step: step_words(), factor: sf_grad_norm's output or None."""
+    _check_words("step", step, torch.int32, tensors.device)
+    if factor is not None:
+        _check_words("factor", factor, torch.float32, tensors.device)
+    _on_current(_one_device(step, factor, status, hp.bc1))
+    h = hp.struct()
+    _check(load().sf_adamw_step(tensors.arr, tensors.n, ctypes.byref(h), _ptr(step), _ptr(factor), _ptr(status),
+                                _stream(stream)), "sf_adamw_step")

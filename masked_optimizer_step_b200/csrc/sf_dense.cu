@@ -1,0 +1,498 @@
+// sf_dense.cu -- AdamW over many dense tensors at once, and the global gradient norm that clips it.
+//
+// The arithmetic is in include/sf.h. Both kernels are single passes over memory: the norm reads
+// every gradient once, the step reads and writes every weight and moment once (28 bytes an element
+// with fp32 moments, a bf16 gradient and a bf16 live copy; 16.06 with 8-bit moments).
+//
+// Layout of the work: a block of 256 elements (the unit that shares the 8-bit moments' scales) belongs to
+// one warp, 8 consecutive elements to a lane, so every access is an 8-, 16- or 32-byte vector of a
+// fully coalesced row and a block's largest magnitude is one warp-wide integer maximum. A unit is
+// `per` blocks for each of a CTA's 8 warps; units of all tensors are numbered through and a CTA
+// takes every gridDim-th one.
+#include <string.h>
+
+#include <cuda_fp8.h>
+
+#include "sf_common.cuh"
+#include "sf_host.h"
+
+namespace sf {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBlock = SF_DENSE_BLOCK;
+constexpr int kLaneElems = kBlock / 32;
+static_assert(kLaneElems == 8, "eight elements to a lane");
+constexpr int kMaxTensors = SF_DENSE_PER_LAUNCH;
+constexpr int kMaxGridPerSm = 8;
+constexpr float kScaleFloor = 0x1p-100f;      // keeps 1 / scale finite
+constexpr float kSmallestCode = 0x1p-9f;      // smallest positive e4m3 value
+
+struct DenseDesc {
+    int64_t n;
+    void *p;
+    const void *g;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    uint16_t *live;
+    float decay;
+    int32_t unit_begin;                       // units of the tensors before this one
+    uint8_t p_type, g_type, state_type, pad;
+};
+
+struct DenseBatch {
+    int32_t n, units, per;                    // tensors, units in all, blocks of a unit per warp
+    DenseDesc d[kMaxTensors];
+};
+static_assert(sizeof(DenseBatch) <= 32000, "kernel parameter space");
+
+struct StepArgs {
+    float beta1, beta2, omb1, omb2, eps, lr, wd, clip;
+    const float *bc1, *bc2;
+    int32_t t_max, last;                      // last: this launch ends the call
+    int32_t *step;
+    const float *factor;
+};
+
+__device__ __forceinline__ int find_tensor(const DenseBatch &b, int unit)
+{
+    int lo = 0, hi = b.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (b.d[mid].unit_begin <= unit) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Up to eight consecutive elements at `at` as fp32 (the first `cnt`; the rest are zero).
+__device__ __forceinline__ void load8(float (&x)[8], const void *base, int type, int64_t at, int cnt)
+{
+    if (type == SF_TYPE_F32) {
+        const float *src = static_cast<const float *>(base) + at;
+        if (cnt == 8) {
+            const float4 a = __ldcs(reinterpret_cast<const float4 *>(src));
+            const float4 c = __ldcs(reinterpret_cast<const float4 *>(src) + 1);
+            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+            x[4] = c.x; x[5] = c.y; x[6] = c.z; x[7] = c.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = e < cnt ? src[e] : 0.0f;
+        }
+        return;
+    }
+    const uint16_t *src = static_cast<const uint16_t *>(base) + at;
+    uint32_t w[4];
+    if (cnt == 8) {
+        const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(src));
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = (2 * e < cnt ? (uint32_t)src[2 * e] : 0u) | (2 * e + 1 < cnt ? (uint32_t)src[2 * e + 1] << 16 : 0u);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (type == SF_TYPE_BF16) {
+            x[2 * e] = __uint_as_float(w[e] << 16);
+            x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        } else {
+            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+            x[2 * e] = h.x;
+            x[2 * e + 1] = h.y;
+        }
+    }
+}
+
+__device__ __forceinline__ void store8_f32(float *dst, const float (&x)[8], int cnt)
+{
+    if (cnt == 8) {
+        __stcs(reinterpret_cast<float4 *>(dst), make_float4(x[0], x[1], x[2], x[3]));
+        __stcs(reinterpret_cast<float4 *>(dst) + 1, make_float4(x[4], x[5], x[6], x[7]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < cnt) dst[e] = x[e];
+    }
+}
+
+__device__ __forceinline__ void store8_bf16(uint16_t *dst, const float (&x)[8], int cnt)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+        w[e] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    if (cnt == 8) {
+        __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(w[0], w[1], w[2], w[3]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < cnt) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+}
+
+// Eight e4m3 codes (zeros behind cnt) as two words.
+__device__ __forceinline__ uint2 load8_codes(const void *base, int64_t at, int cnt)
+{
+    const uint8_t *src = static_cast<const uint8_t *>(base) + at;
+    if (cnt == 8) return __ldcs(reinterpret_cast<const uint2 *>(src));
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < cnt) w[e >> 2] |= (uint32_t)src[e] << (8 * (e & 3));
+    return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ void decode8(float (&x)[8], uint2 codes, float scale)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t w = e < 2 ? codes.x : codes.y;
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * (e & 1))), __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        x[2 * e] = __fmul_rn(f.x, scale);
+        x[2 * e + 1] = __fmul_rn(f.y, scale);
+    }
+}
+
+// Codes and scale of a block's values (this lane's eight); POSITIVE values keep a positive code.
+template <bool POSITIVE>
+__device__ __forceinline__ void encode8(const float (&x)[8], void *base, int64_t at, int cnt, float *scale, int lane)
+{
+    uint32_t big = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) big = max(big, __float_as_uint(fabsf(x[e])));
+    big = __reduce_max_sync(0xffffffffu, big);       // magnitudes order as their bits; a NaN is the largest
+    float sc = __fmul_rn(__uint_as_float(big), 1.0f / 448.0f);
+    if (sc < kScaleFloor) sc = kScaleFloor;          // a NaN stays
+    const float inv = __frcp_rn(sc);
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float a = __fmul_rn(x[2 * e], inv), b = __fmul_rn(x[2 * e + 1], inv);
+        if (POSITIVE) {
+            if (x[2 * e] > 0.0f && a < kSmallestCode) a = kSmallestCode;
+            if (x[2 * e + 1] > 0.0f && b < kSmallestCode) b = kSmallestCode;
+        }
+        w[e >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) << (16 * (e & 1));
+    }
+    uint8_t *dst = static_cast<uint8_t *>(base) + at;
+    if (cnt == 8) {
+        __stcs(reinterpret_cast<uint2 *>(dst), make_uint2(w[0], w[1]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < cnt) dst[e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+    }
+    if (lane == 0) *scale = sc;
+}
+
+__global__ void __launch_bounds__(kThreads)
+adamw_kernel(const __grid_constant__ DenseBatch b, const StepArgs a, uint32_t *status)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = a.step[0] + 1;
+    const float f = a.factor ? a.factor[1] : 1.0f;
+    if (!(f != 0.0f) || f != f) {                    // the gradient was not finite: leave everything
+        if (blockIdx.x == 0 && threadIdx.x == 0) set_status(status, SF_STATUS_NONFINITE);
+        return;
+    }
+    const int ti = t < 0 ? 0 : t < a.t_max ? t : a.t_max;
+    const float bc1 = a.bc1[ti], root2 = __fsqrt_rn(a.bc2[ti]);
+    float nan_sum = 0.0f;                            // stays 0 while everything is finite
+
+    for (int unit = blockIdx.x; unit < b.units; unit += gridDim.x) {
+        const DenseDesc &d = b.d[find_tensor(b, unit)];
+        const int64_t first = (int64_t)(unit - d.unit_begin) * b.per * kWarps;     // the unit's first block
+        const float wd = __fmul_rn(d.decay, __fmul_rn(a.lr, a.wd));
+        for (int k = 0; k < b.per; ++k) {
+            const int64_t blk = first + (int64_t)k * kWarps + warp;
+            const int64_t at = blk * kBlock + lane * kLaneElems;
+            if (blk * kBlock >= d.n) break;
+            const int cnt = (int)max((int64_t)0, min((int64_t)8, d.n - at));
+            float p[8], g[8], m[8], v[8];
+            const bool coded = d.state_type == SF_TYPE_E4M3;
+            load8(p, d.p, d.p_type, at, cnt);
+            load8(g, d.g, d.g_type, at, cnt);
+            if (coded) {
+                const uint2 cm = load8_codes(d.m, at, cnt), cv = load8_codes(d.v, at, cnt);
+                decode8(m, cm, d.m_scale[blk]);
+                decode8(v, cv, d.v_scale[blk]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], v[e]);
+            } else {
+                load8(m, d.m, SF_TYPE_F32, at, cnt);
+                load8(v, d.v, SF_TYPE_F32, at, cnt);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float x = __fmul_rn(g[e], f);
+                if (a.clip > 0.0f) x = fminf(fmaxf(x, -a.clip), a.clip);
+                m[e] = __fadd_rn(__fmul_rn(m[e], a.beta1), __fmul_rn(x, a.omb1));
+                v[e] = __fadd_rn(__fmul_rn(v[e], a.beta2), __fmul_rn(__fmul_rn(x, x), a.omb2));
+                const float root = __fsqrt_rn(v[e]);
+                const float u = __fdiv_rn(__fmul_rn(m[e], bc1), __fmaf_rn(root, root2, a.eps));
+                p[e] = __fmaf_rn(-wd, p[e], __fmaf_rn(-a.lr, u, p[e]));
+                if (e < cnt) nan_sum = __fmaf_rn(v[e], 0.0f, __fmaf_rn(p[e], 0.0f, nan_sum));
+                if (coded) v[e] = root;
+            }
+            if (d.p_type == SF_TYPE_F32) store8_f32(static_cast<float *>(d.p) + at, p, cnt);
+            else store8_bf16(static_cast<uint16_t *>(d.p) + at, p, cnt);
+            if (d.live) store8_bf16(d.live + at, p, cnt);
+            if (coded) {
+                encode8<false>(m, d.m, at, cnt, d.m_scale + blk, lane);
+                encode8<true>(v, d.v, at, cnt, d.v_scale + blk, lane);
+            } else {
+                store8_f32(static_cast<float *>(d.m) + at, m, cnt);
+                store8_f32(static_cast<float *>(d.v) + at, v, cnt);
+            }
+        }
+    }
+    if (nan_sum != 0.0f) set_status(status, SF_STATUS_NONFINITE);
+    // The last CTA to finish counts the step: by then every CTA has read the old count.
+    if (a.last) {
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            __threadfence();
+            if (atomicAdd(a.step + 1, 1) == (int)gridDim.x - 1) {
+                a.step[0] = t;
+                a.step[1] = 0;
+            }
+        }
+    }
+}
+
+// A call with no elements still counts a step.
+__global__ void count_step_kernel(int32_t *step, const float *factor, uint32_t *status)
+{
+    const float f = factor ? factor[1] : 1.0f;
+    if (f != 0.0f && f == f) step[0] += 1;
+    else set_status(status, SF_STATUS_NONFINITE);
+}
+
+// ws of the norm: [0] CTAs that have finished (int32, 0 between calls), then a double per CTA.
+constexpr size_t kNormHeader = 16;
+
+// Sum of squares: fp32 over a lane's eight elements, fp64 from there. Every CTA leaves its sum in its own
+// place; the last one of the call adds them in a fixed order.
+__global__ void __launch_bounds__(kThreads)
+grad_norm_kernel(const __grid_constant__ DenseBatch b, int32_t *done, double *sums, int at0, int total_ctas,
+                 float inv_scale, float max_norm, float *out, uint32_t *status)
+{
+    __shared__ double part[kWarps];
+    __shared__ int is_last;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    double sum = 0.0;
+    for (int unit = blockIdx.x; unit < b.units; unit += gridDim.x) {
+        const DenseDesc &d = b.d[find_tensor(b, unit)];
+        const int64_t first = (int64_t)(unit - d.unit_begin) * b.per * kWarps;
+#pragma unroll 4
+        for (int k = 0; k < b.per; ++k) {
+            const int64_t at = (first + (int64_t)k * kWarps + warp) * kBlock + lane * kLaneElems;
+            const int cnt = (int)max((int64_t)0, min((int64_t)8, d.n - at));
+            float g[8];
+            load8(g, d.g, d.g_type, at, cnt);
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = __fmaf_rn(g[e], g[e], s);
+            sum += (double)s;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) part[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double s = 0.0;
+        for (int w = 0; w < kWarps; ++w) s += part[w];
+        sums[at0 + blockIdx.x] = s;
+        __threadfence();
+        is_last = atomicAdd(done, 1) == total_ctas - 1;
+    }
+    __syncthreads();
+    if (!is_last) return;
+    __threadfence();
+    sum = 0.0;
+    for (int i = threadIdx.x; i < total_ctas; i += kThreads) sum += __ldcg(sums + i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    __syncthreads();
+    if (lane == 0) part[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double s = 0.0;
+        for (int w = 0; w < kWarps; ++w) s += part[w];
+        const float norm = (float)(sqrt(s) * (double)inv_scale);
+        float f = inv_scale;
+        if (max_norm > 0.0f) f = __fmul_rn(inv_scale, fminf(1.0f, __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f))));
+        if (!isfinite(norm)) {
+            f = 0.0f;
+            set_status(status, SF_STATUS_NONFINITE);
+        }
+        out[0] = norm;
+        out[1] = f;
+        *done = 0;
+    }
+}
+
+// ------------------------------------ host side ------------------------------------
+
+int check_dense(const sf_dense *t, int n, bool step)
+{
+    if (n < 0 || (n > 0 && !t)) return SF_ERR_ARG;
+    for (int i = 0; i < n; ++i) {
+        const sf_dense &a = t[i];
+        if (a.n < 0) return SF_ERR_ARG;
+        if (a.g_type != SF_TYPE_F32 && a.g_type != SF_TYPE_BF16 && a.g_type != SF_TYPE_F16) return SF_ERR_ARG;
+        if (a.n > 0 && !a.g) return SF_ERR_ARG;
+        if (!aligned16(a.g)) return SF_ERR_ALIGN;
+        if (!step) continue;
+        if (a.p_type != SF_TYPE_F32 && a.p_type != SF_TYPE_BF16) return SF_ERR_ARG;
+        if (a.state_type != SF_TYPE_F32 && a.state_type != SF_TYPE_E4M3) return SF_ERR_ARG;
+        if (a.n > 0 && (!a.p || !a.m || !a.v)) return SF_ERR_ARG;
+        if (a.n > 0 && a.state_type == SF_TYPE_E4M3 && (!a.m_scale || !a.v_scale)) return SF_ERR_ARG;
+        if (!aligned16(a.p) || !aligned16(a.m) || !aligned16(a.v) || !aligned16(a.live)) return SF_ERR_ALIGN;
+        if (((uintptr_t)a.m_scale & 3) || ((uintptr_t)a.v_scale & 3)) return SF_ERR_ALIGN;
+    }
+    return SF_OK;
+}
+
+// Blocks of a unit per warp: long units amortise finding the tensor and keep loads in flight, short ones
+// spread a small call over the SMs.
+int unit_blocks(const sf_dense *t, int n, int sms)
+{
+    int64_t blocks = 0;
+    for (int i = 0; i < n; ++i) blocks += (t[i].n + kBlock - 1) / kBlock;
+    const int64_t each = blocks / ((int64_t)sms * kWarps * kMaxGridPerSm);
+    return each >= 8 ? 8 : each >= 4 ? 4 : each >= 2 ? 2 : 1;
+}
+
+// The next launch's tensors, from *at on. Returns the units, or -1 when they pass 2^31.
+int64_t fill(DenseBatch &b, const sf_dense *t, int n, int *at, int per)
+{
+    b.n = 0;
+    b.per = per;
+    int64_t units = 0;
+    for (; *at < n && b.n < kMaxTensors; ++*at) {
+        const sf_dense &a = t[*at];
+        if (a.n == 0) continue;
+        DenseDesc &d = b.d[b.n++];
+        d.n = a.n;
+        d.p = a.p;
+        d.g = a.g;
+        d.m = a.m;
+        d.v = a.v;
+        d.m_scale = a.m_scale;
+        d.v_scale = a.v_scale;
+        d.live = a.live;
+        d.decay = a.decay;
+        d.p_type = (uint8_t)a.p_type;
+        d.g_type = (uint8_t)a.g_type;
+        d.state_type = (uint8_t)a.state_type;
+        d.pad = 0;
+        d.unit_begin = (int32_t)units;
+        units += (a.n + (int64_t)per * kWarps * kBlock - 1) / ((int64_t)per * kWarps * kBlock);
+        if (units > INT32_MAX / 2) return -1;
+    }
+    b.units = (int32_t)units;
+    return units;
+}
+
+int count_launches(const sf_dense *t, int n)
+{
+    int full = 0;
+    for (int i = 0; i < n; ++i) full += t[i].n > 0;
+    return (full + kMaxTensors - 1) / kMaxTensors;
+}
+
+}  // namespace
+}  // namespace sf
+
+using namespace sf;
+
+extern "C" size_t sf_grad_norm_ws_bytes(const sf_dense *t, int n)
+{
+    if (n < 0 || (n > 0 && !t)) return 0;
+    const int launches = count_launches(t, n);
+    // a place for every CTA of every launch, on a device of up to 256 SMs
+    return kNormHeader + (size_t)(launches > 0 ? launches : 1) * 256 * kMaxGridPerSm * sizeof(double);
+}
+
+extern "C" int sf_grad_norm(const sf_dense *t, int n, float inv_scale, float max_norm, float *out, void *ws,
+                            size_t ws_bytes, uint32_t *dev_status, sf_stream stream)
+{
+    int rc = check_dense(t, n, false);
+    if (rc != SF_OK) return rc;
+    if (!out || !ws || !(inv_scale > 0.0f) || max_norm != max_norm) return SF_ERR_ARG;
+    if (ws_bytes < sf_grad_norm_ws_bytes(t, n)) return SF_ERR_ARG;
+    if (!aligned16(ws) || ((uintptr_t)out & 3)) return SF_ERR_ALIGN;
+    const int sms = sm_count();
+    if (sms <= 0) return SF_ERR_NO_DEVICE;
+    if (sms > 256) return SF_ERR_UNSUPPORTED;
+    const int per = unit_blocks(t, n, sms);
+    const int64_t cap = (int64_t)sms * kMaxGridPerSm;
+    DenseBatch b;
+    // the CTAs of all launches, so that the last one of them knows itself
+    int64_t total = 0;
+    for (int at = 0, first = 1; first || at < n; first = 0) {
+        const int64_t units = fill(b, t, n, &at, per);
+        if (units < 0) return SF_ERR_UNSUPPORTED;
+        if (units > 0 || first) total += units < cap ? (units > 0 ? units : 1) : cap;
+    }
+    int32_t *done = static_cast<int32_t *>(ws);
+    double *sums = reinterpret_cast<double *>(static_cast<char *>(ws) + kNormHeader);
+    int64_t placed = 0;
+    for (int at = 0, first = 1; first || at < n; first = 0) {
+        const int64_t units = fill(b, t, n, &at, per);
+        if (units == 0 && !first) continue;
+        const int64_t grid = units < cap ? (units > 0 ? units : 1) : cap;
+        grad_norm_kernel<<<(int)grid, kThreads, 0, as_stream(stream)>>>(b, done, sums, (int)placed, (int)total,
+                                                                       inv_scale, max_norm, out, dev_status);
+        if (launch_status() != SF_OK) return SF_ERR_CUDA;
+        placed += grid;
+    }
+    return SF_OK;
+}
+
+extern "C" int sf_adamw_step(const sf_dense *t, int n, const sf_adam *hp, int32_t *step, const float *factor,
+                             uint32_t *dev_status, sf_stream stream)
+{
+    int rc = check_dense(t, n, true);
+    if (rc != SF_OK) return rc;
+    if (!hp || !hp->bc1 || !hp->bc2 || hp->t_max < 1 || !step) return SF_ERR_ARG;
+    if (((uintptr_t)step & 3) || ((uintptr_t)factor & 3)) return SF_ERR_ALIGN;
+    const int sms = sm_count();
+    if (sms <= 0) return SF_ERR_NO_DEVICE;
+    StepArgs a;
+    a.beta1 = hp->beta1;
+    a.beta2 = hp->beta2;
+    a.omb1 = hp->one_minus_b1;
+    a.omb2 = hp->one_minus_b2;
+    a.eps = hp->eps;
+    a.lr = hp->lr;
+    a.wd = hp->wd;
+    a.clip = hp->clip;
+    a.bc1 = hp->bc1;
+    a.bc2 = hp->bc2;
+    a.t_max = hp->t_max;
+    a.step = step;
+    a.factor = factor;
+    const int launches = count_launches(t, n);
+    if (launches == 0) {
+        count_step_kernel<<<1, 1, 0, as_stream(stream)>>>(step, factor, dev_status);
+        return launch_status();
+    }
+    const int per = unit_blocks(t, n, sms);
+    DenseBatch b;
+    for (int at = 0, li = 0; li < launches; ++li) {
+        const int64_t units = fill(b, t, n, &at, per);
+        if (units < 0) return SF_ERR_UNSUPPORTED;
+        a.last = li == launches - 1;
+        const int64_t cap = (int64_t)sms * kMaxGridPerSm;
+        adamw_kernel<<<(int)(units < cap ? units : cap), kThreads, 0, as_stream(stream)>>>(b, a, dev_status);
+        if (launch_status() != SF_OK) return SF_ERR_CUDA;
+    }
+    return SF_OK;
+}
