@@ -441,6 +441,51 @@ int sf_grad_norm(const sf_dense *t /* host [n] */, int n, float inv_scale, float
 int sf_adamw_step(const sf_dense *t /* host [n] */, int n, const sf_adam *hp, int32_t *step,
                   const float *factor, uint32_t *dev_status, sf_stream stream);
 
+/* ---- sf_grouped_forward / sf_grouped_dx / sf_grouped_dw: products grouped by expert --------------
+ * No counterpart in the paper: the forward pass and the dense gradients of a layer of E experts, each
+ * with a weight matrix W[e] [R x C] of its own. The rows of A and Y are tokens (a token sent to several
+ * experts has a row for each), sorted by expert: expert e owns rows offsets[e] .. offsets[e+1]-1, which
+ * may be none. The offsets live on the device, so a router's counts need not come to the host.
+ *   sf_grouped_forward   Y[t, r]    = sum_c A[t, c] * W[e, r, c]          writes Y
+ *   sf_grouped_dx        A[t, c]    = sum_r Y[t, r] * W[e, r, c]          writes A (the input gradient)
+ *   sf_grouped_dw        W[e, r, c] = sum_t Y[t, r] * A[t, c]             writes W (the weight gradient)
+ * for every t of expert e, accumulated in fp32 on the tensor cores and rounded once. A and Y are bf16 or
+ * fp16 (`type`); W is of the same type, or fp32 for the weight gradient (w_type).
+ * Rows of the written operand outside offsets[0] .. offsets[E]-1 are left as they were. An expert
+ * without tokens gets a zero weight gradient; with `accumulate` (fp32 W only) the weight gradient is
+ * added to what W holds, and an expert without tokens keeps it. A non-finite value reaches only the
+ * results whose sums hold it.
+ * offsets must not fall and must lie in [0, T]: otherwise nothing is computed and SF_STATUS_BAD_OFFSET is
+ * set. Pipeline waits are bounded as in sf_masked_dw (SF_STATUS_WAIT_TIMEOUT).
+ * Deterministic: every result is summed by one CTA (or by a cluster in a fixed order), and which rows
+ * share a tile changes no sum. Requirements: 1 <= E <= 1024; T >= 0; R, C positive multiples of 8;
+ * ld_a >= C, ld_y >= R, ld_w >= C, stride_w >= (R - 1) * ld_w + C when E > 1; strides multiples of 8 elements
+ * (4 for an fp32 W); A, W, Y 16-byte aligned (A and Y may be NULL when T = 0). One launch a call.
+ * Errors: SF_ERR_ARG, SF_ERR_ALIGN, SF_ERR_UNSUPPORTED (E above 1024, or more than 2^30 tiles).
+ */
+#define SF_GROUPED_MAX_EXPERTS 1024
+
+typedef struct sf_grouped {
+    void          *A;         /* [T x ld_a] */
+    int64_t        ld_a;
+    void          *W;         /* [E x stride_w], rows ld_w apart */
+    int64_t        ld_w;
+    int64_t        stride_w;
+    void          *Y;         /* [T x ld_y] */
+    int64_t        ld_y;
+    const int32_t *offsets;   /* device [E + 1] */
+    int32_t        E;
+    int32_t        T;
+    int32_t        R;
+    int32_t        C;
+    int32_t        type;
+    int32_t        w_type;
+} sf_grouped;
+
+int sf_grouped_forward(const sf_grouped *p /* host */, uint32_t *dev_status, sf_stream stream);
+int sf_grouped_dx(const sf_grouped *p /* host */, uint32_t *dev_status, sf_stream stream);
+int sf_grouped_dw(const sf_grouped *p /* host */, int accumulate, uint32_t *dev_status, sf_stream stream);
+
 /* ---- helpers (not on the hot path) ------------------------------------------------------ */
 
 /* Quantise a full-precision matrix into the int8 + scale + residual storage of section 2.3

@@ -39,6 +39,7 @@ SF_TYPE_F16 = 2
 SF_TYPE_E4M3 = 3
 SF_DENSE_BLOCK = 256
 SF_DENSE_PER_LAUNCH = 384
+SF_GROUPED_MAX_EXPERTS = 1024
 
 SF_DW_MAX_PER_LAUNCH = 96
 SF_MASKS_PER_LAUNCH = 240
@@ -93,6 +94,11 @@ class sf_dense(ctypes.Structure):
                 ("live", _P), ("decay", _F), ("p_type", _I32), ("g_type", _I32), ("state_type", _I32)]
 
 
+class sf_grouped(ctypes.Structure):
+    _fields_ = [("A", _P), ("ld_a", _I64), ("W", _P), ("ld_w", _I64), ("stride_w", _I64), ("Y", _P), ("ld_y", _I64),
+                ("offsets", _P), ("E", _I32), ("T", _I32), ("R", _I32), ("C", _I32), ("type", _I32), ("w_type", _I32)]
+
+
 _lib = None
 
 
@@ -139,7 +145,10 @@ def load():
     L.sf_grad_norm_ws_bytes.argtypes = [ctypes.POINTER(sf_dense), ctypes.c_int]
     L.sf_grad_norm.argtypes = [ctypes.POINTER(sf_dense), ctypes.c_int, _F, _F, _P, _P, ctypes.c_size_t, _P, _P]
     L.sf_adamw_step.argtypes = [ctypes.POINTER(sf_dense), ctypes.c_int, ctypes.POINTER(sf_adam), _P, _P, _P, _P]
-    for name in ("sf_grad_norm", "sf_adamw_step"):
+    L.sf_grouped_forward.argtypes = [ctypes.POINTER(sf_grouped), _P, _P]
+    L.sf_grouped_dx.argtypes = [ctypes.POINTER(sf_grouped), _P, _P]
+    L.sf_grouped_dw.argtypes = [ctypes.POINTER(sf_grouped), ctypes.c_int, _P, _P]
+    for name in ("sf_grad_norm", "sf_adamw_step", "sf_grouped_forward", "sf_grouped_dx", "sf_grouped_dw"):
         getattr(L, name).restype = ctypes.c_int
     for name in ("sf_mask_init", "sf_mask_update", "sf_masked_dw", "sf_embed_grad", "sf_adam_tables",
                  "sf_sparse_update", "sf_quantize_init", "sf_mask_update_phase", "sf_masked_dw_phase",
@@ -558,3 +567,58 @@ def sf_adamw_step(tensors: DenseTensors, hp: AdamParams, step, factor=None, stat
     h = hp.struct()
     _check(load().sf_adamw_step(tensors.arr, tensors.n, ctypes.byref(h), _ptr(step), _ptr(factor), _ptr(status),
                                 _stream(stream)), "sf_adamw_step")
+
+
+# ---------------------------------------------------------------------------------------------
+# Products grouped by expert
+# ---------------------------------------------------------------------------------------------
+
+def grouped_problem(A, W, Y, offsets) -> Desc:
+    """The operands of sf_grouped_forward (writes Y), sf_grouped_dx (writes A) or sf_grouped_dw (writes W).
+
+    A [T x C] and Y [T x R] bf16 or fp16, rows sorted by expert; W [E x R x C] of the same type (fp32 or
+    that type for the weight gradient); offsets int32 [E + 1] on the device: expert e owns rows
+    offsets[e] .. offsets[e+1]-1. Rows may be strided, columns not."""
+    if A.dim() != 2 or Y.dim() != 2 or W.dim() != 3:
+        raise ValueError("A [T x C], W [E x R x C] and Y [T x R] expected")
+    (T, C), (E, R) = A.shape, W.shape[:2]
+    if W.shape[2] != C or tuple(Y.shape) != (T, R):
+        raise ValueError(f"shapes do not match: A {tuple(A.shape)}, W {tuple(W.shape)}, Y {tuple(Y.shape)}")
+    for name, t in (("A", A), ("W", W), ("Y", Y)):
+        if t.numel() and t.stride(-1) != 1:
+            raise ValueError(f"{name}: columns must be contiguous")
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() != E + 1 or not offsets.is_contiguous():
+        raise ValueError(f"offsets: {E + 1} contiguous int32 expected")
+    ty = _type(A, (SF_TYPE_BF16, SF_TYPE_F16), "A")
+    wt = _type(W, (ty, SF_TYPE_F32), "W")
+    _type(Y, (ty,), "Y")
+    _one_device(A, W, Y, offsets)
+    # a single row's or matrix's stride says nothing: give the dense one
+    ld_a = A.stride(0) if T > 1 else max(A.stride(0), C)
+    ld_y = Y.stride(0) if T > 1 else max(Y.stride(0), R)
+    ld_w = W.stride(1) if R > 1 else max(W.stride(1), C)
+    stride_w = W.stride(0) if E > 1 else R * ld_w
+    c = sf_grouped(_ptr(A) or None, ld_a, _ptr(W), ld_w, stride_w, _ptr(Y) or None, ld_y, _ptr(offsets), E, T, R, C,
+                   ty, wt)
+    return Desc(c, A, W, Y, offsets)
+
+
+def _grouped(name, p: Desc, status, stream, *extra):
+    _on_current(p.refs[1].device.index)
+    _check(getattr(load(), name)(ctypes.byref(p.c), *extra, _ptr(status), _stream(stream)), name)
+
+
+def sf_grouped_forward(p: Desc, status=None, stream=None):
+    """Y[t] = W[e(t)] A[t] for every expert's rows."""
+    _grouped("sf_grouped_forward", p, status, stream)
+
+
+def sf_grouped_dx(p: Desc, status=None, stream=None):
+    """A[t] = W[e(t)]^T Y[t]: the input gradient, with Y the gradient of the outputs."""
+    _grouped("sf_grouped_dx", p, status, stream)
+
+
+def sf_grouped_dw(p: Desc, status=None, stream=None, accumulate: bool = False):
+    """W[e] = sum over e's tokens of Y[t] A[t]^T: the weight gradient, with Y the gradient of the outputs;
+    accumulate adds it to what W (fp32) holds."""
+    _grouped("sf_grouped_dw", p, status, stream, int(accumulate))

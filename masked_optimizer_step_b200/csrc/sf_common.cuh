@@ -297,6 +297,18 @@ SF_DEVICE void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32])
         : "r"(taddr));
 }
 
+// The 16-column form.
+SF_DEVICE void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
 SF_DEVICE void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // --------------------------------------------------------------------------------------------
@@ -317,6 +329,42 @@ SF_DEVICE void mbar_arrive_remote(uint64_t *bar, uint32_t rank)
                  "mapa.shared::cluster.u32 ra, %0, %1;\n\t"
                  "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra];\n\t}"
                  ::"r"(smem_u32(bar)), "r"(rank) : "memory");
+}
+
+// mbar_wait whose phase was (partly) completed by arrivals from the cluster's other CTA: what those
+// threads wrote before they arrived is visible after it.
+SF_DEVICE bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+        if (ok) return true;
+        if (*abort) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
+// What this thread wrote to shared memory with ordinary stores is visible to the tensor cores and TMA.
+SF_DEVICE void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// The address of the caller's shared-memory location in CTA `rank` of the cluster, and a store to one.
+SF_DEVICE uint32_t mapa_u32(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+SF_DEVICE void st_cluster_u32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // Every thread of every CTA of the cluster arrives, then waits for all of them.
