@@ -260,6 +260,16 @@ SF_DEVICE void tmem_dealloc(uint32_t taddr, uint32_t ncols)
                  : "memory");
 }
 
+// True in one lane of a converged warp. Code that every lane runs with one thread elected at the tcgen05
+// instruction keeps descriptors in uniform registers; a loop that one lane runs alone does not (grouped forward
+// on 256 x 256 pair tiles, no loads: 177 cycles an MMA that takes 128).
+SF_DEVICE bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // D[tmem] (+)= A[smem] * B[smem], kind::f16 (bf16 inputs, fp32 accumulate), one thread.
 SF_DEVICE void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                         uint32_t accumulate)
@@ -353,6 +363,43 @@ SF_DEVICE bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *a
 
 // What this thread wrote to shared memory with ordinary stores is visible to the tensor cores and TMA.
 SF_DEVICE void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Barrier `id` of `threads` threads; true for all of them when `ok` is true for all of them.
+SF_DEVICE bool bar_all(int id, int threads, bool ok)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+                 "barrier.cta.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"(id), "r"(threads), "r"((uint32_t)ok) : "memory");
+    return r != 0;
+}
+
+// Bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) from shared to global memory, in the
+// calling thread's current bulk group.
+SF_DEVICE void bulk_store(void *dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
+
+// 3-D tiled TMA store of a box {x, y, z} from shared memory, or its addition (fp32) to what is there.
+SF_DEVICE void tma_store_3d(const CUtensorMap *m, const void *src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)) : "memory");
+}
+
+SF_DEVICE void tma_add_3d(const CUtensorMap *m, const void *src, int x, int y, int z)
+{
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)) : "memory");
+}
+
+SF_DEVICE void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// All but the thread's N latest bulk groups have read their shared memory; all its groups are complete.
+template <int N>
+SF_DEVICE void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+SF_DEVICE void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // The address of the caller's shared-memory location in CTA `rank` of the cluster, and a store to one.
 SF_DEVICE uint32_t mapa_u32(uint32_t addr, uint32_t rank)

@@ -25,18 +25,26 @@ constexpr int GK = 64;                        // elements of K per stage: 128 by
 constexpr int G_UMMA_K = 16;
 constexpr int G_BOX_BYTES = 64 * GK * 2;      // a 64 x 64 box
 
-// ---- tiles of CTA pairs: 256 accumulator rows x up to 256 columns, both CTAs' MMAs as one (cta_group::2) ----
+// ---- tiles of CTA pairs: 256 accumulator rows x up to 512 columns, both CTAs' MMAs as one (cta_group::2). The columns
+// are two halves of up to 256, two MMAs that share a stage's M operand: a stage of 48 KB in each SM then keeps the
+// tensor cores busy for 1,024 cycles, so 4 of them cover the 2 us that a stage takes from its release to its next use
+// (pairs of 256 x 256 with 32 KB stages: 512 cycles, and 1.4 us with nothing else on the memory system). ----
 constexpr int PM = 256;                       // accumulator rows of a pair, 128 in each CTA's TMEM
-constexpr int PN = 256;                       // accumulator columns at most
-constexpr int P_STAGES = 6;
-constexpr int P_HALF_BYTES = 128 * GK * 2;    // one operand of a stage in one CTA: 16 KB
-constexpr int P_STAGE_BYTES = 2 * P_HALF_BYTES;
-constexpr int P_NBUF = 2;                     // accumulators: the MMAs fill one while the epilogue drains the other
-constexpr int P_TMEM_COLS = P_NBUF * PN;
+constexpr int PN = 256;                       // columns of a half, at most
+constexpr int P_HALF_BYTES = 128 * GK * 2;    // 128 rows of an operand, a stage, in one CTA: 16 KB
+constexpr int P_TMEM_COLS = 2 * PN;
 constexpr int P_EPI_WARPS = 8;                // two per TMEM lane quarter
 constexpr int P_THREADS = 64 + 32 * P_EPI_WARPS;
-constexpr size_t P_SMEM_BYTES = (size_t)P_STAGES * P_STAGE_BYTES + 1024;
-constexpr int P_BAND = 8;                     // token tiles that share a pass over an expert's weights
+constexpr int W_THREADS = P_THREADS + 32;     // weight gradient: and a warp that clears rows
+constexpr int T_TOKENS = 2 * PN;              // columns of a tile, at most
+constexpr int T_STAGES = 4;
+constexpr int T_STAGE_BYTES = 3 * P_HALF_BYTES;
+constexpr int T_OUT_BYTES = 32 * 128 * 2;     // forward, dx: 32 tokens' rows of the CTA's 128 features, on their way out
+constexpr int W_OUT_BYTES = 32 * 128;         // weight gradient: 32 rows of 128 bytes of a warp's output
+constexpr size_t T_SMEM_BYTES = (size_t)T_STAGES * T_STAGE_BYTES + 2 * T_OUT_BYTES + 1024;
+constexpr size_t W_SMEM_BYTES = (size_t)T_STAGES * T_STAGE_BYTES + P_EPI_WARPS * W_OUT_BYTES + 1024;
+constexpr int T_AHEAD = 3;                    // stages of a unit whose first halves run before any second half
+constexpr int T_BAND = 4;                     // token tiles that share a pass over an expert's weights
 
 // ---- single CTAs: 128 accumulator rows x up to 128 columns, K split over a cluster ----
 constexpr int SM_ROWS = 128;
@@ -45,14 +53,23 @@ constexpr int S_THREADS = 64 + 32 * S_EPI_WARPS;
 constexpr int S_W_BYTES = SM_ROWS * GK * 2;   // 16 KB
 constexpr int S_MAX_STAGES = 12;
 
-constexpr int W_CHUNK_STAGES = 1024 / GK;     // weight gradient: tokens summed by the tensor core before fp32 adds
+
+// Weight gradient, fp32: tokens that the tensor core sums before the sums are added in fp32, in stages. It adds with
+// truncation, so the error grows with the length (relative, normal values: 2.3e-7, 9.9e-7 and 9.1e-6 at 256, 1,024
+// and 8,192 tokens); 960 keep it below 1e-6 at any length.
+constexpr int W_CHUNK_STAGES = 960 / GK;
+
+// Tokens to a tile, at most, that the pair kernel chooses from.
+constexpr int kCands = 15;
+__device__ __forceinline__ int cand_tokens(int i) { return T_TOKENS - 32 * i; }      // 512 .. 64
 
 struct GArgs {
     CUtensorMap tm_w;          // forward, dx: W as {C, R, E}; dw: A as {C, T}
     CUtensorMap tm_x;          // tokens: forward A, dx Y as {K, T}; dw: Y as {R, T}
+    CUtensorMap tm_out;        // dw: W as {C, R, E}, boxes of 128 bytes x 32 rows
     const int32_t *offsets;
-    void *out;
-    int64_t ld_out, stride_out;
+    void *out;                 // forward, dx
+    int64_t ld_out;
     int32_t E, T, M, K, type;  // M: accumulator rows in all (forward R, dx C, dw R); K: forward C, dx R, dw C (its N)
     int32_t nb, stages, ksplit;      // single CTAs: token box, stages, CTAs of a cluster
     int32_t out_f32, accumulate;     // dw
@@ -86,36 +103,72 @@ __device__ __forceinline__ int tile_tokens(int cnt, int most, int step)
 
 struct Plan {
     int off[kMaxE + 1];        // offsets
-    int pre[kMaxE + 1];        // units of the experts before
+    int pre[kMaxE + 1];        // units of the experts before, in the order below
+    uint16_t order[kMaxE];     // experts in the order in which their units are numbered
     int scratch[33];
+    int cand_units[kCands], cand_cost[kCands];
+    int most;                  // tokens to a tile, at most
 };
 
-// Offsets and unit counts into shared memory. False (for every thread) when the offsets are not valid.
-// per_expert(tokens) -> units. Contains __syncthreads.
-template <typename F>
-__device__ __forceinline__ bool load_plan(Plan &pl, const int32_t *offsets, int E, int T, F per_expert)
+// Offsets into shared memory. False (for every thread) when they are not valid. Contains __syncthreads.
+__device__ __forceinline__ bool load_offsets(Plan &pl, const int32_t *offsets, int E, int T)
 {
-    int run = 0, bad = 0;
-    for (int base = 0; base < E; base += blockDim.x) {
-        const int e = base + threadIdx.x;
-        int units = 0;
-        if (e < E) {
-            const int o0 = offsets[e], o1 = offsets[e + 1];
-            if (o0 < 0 || o1 < o0 || o1 > T) bad = 1;
-            else units = per_expert(o1 - o0);
-            pl.off[e] = o0;
-            if (e == E - 1) pl.off[E] = o1;
-        }
-        int total;
-        const int at = block_exclusive_scan(units, pl.scratch, &total);
-        if (e < E) pl.pre[e] = run + at;
-        run += total;
+    int bad = 0;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        const int o0 = offsets[e], o1 = offsets[e + 1];
+        if (o0 < 0 || o1 < o0 || o1 > T) bad = 1;
+        pl.off[e] = o0;
+        if (e == E - 1) pl.off[E] = o1;
     }
-    if (threadIdx.x == 0) pl.pre[E] = run;
     return !__syncthreads_or(bad);
 }
 
-__device__ __forceinline__ int find_expert(const Plan &pl, int E, int u)
+// Experts by falling key (their own order among equals): long units first, so that the last ones to finish are
+// short. Beyond kSortE experts the units are short beside the whole and keep the experts' order: ranking them, E
+// reads a thread for each E / blockDim.x experts, would cost more than it evens out. Contains __syncthreads.
+constexpr int kSortE = 256;
+template <typename F>
+__device__ __forceinline__ void order_experts(Plan &pl, int E, F key)
+{
+    int *keys = pl.pre;                       // free until the units are counted
+    if (E <= kSortE)
+        for (int e = threadIdx.x; e < E; e += blockDim.x) keys[e] = key(pl.off[e + 1] - pl.off[e]);
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        int rank = e;
+        if (E <= kSortE) {
+            const int mine = keys[e];
+            rank = 0;
+            for (int k = 0; k < E; ++k) rank += keys[k] > mine || (keys[k] == mine && k < e);
+        }
+        pl.order[rank] = (uint16_t)e;
+    }
+    __syncthreads();
+}
+
+// Unit counts of the experts in order: per_expert(tokens) -> units. Contains __syncthreads.
+template <typename F>
+__device__ __forceinline__ void count_units(Plan &pl, int E, F per_expert)
+{
+    int run = 0;
+    for (int base = 0; base < E; base += blockDim.x) {
+        const int i = base + threadIdx.x;
+        int units = 0;
+        if (i < E) {
+            const int e = pl.order[i];
+            units = per_expert(pl.off[e + 1] - pl.off[e]);
+        }
+        int total;
+        const int at = block_exclusive_scan(units, pl.scratch, &total);
+        if (i < E) pl.pre[i] = run + at;
+        run += total;
+    }
+    if (threadIdx.x == 0) pl.pre[E] = run;
+    __syncthreads();
+}
+
+// The place in the order of the expert that unit u belongs to.
+__device__ __forceinline__ int find_place(const Plan &pl, int E, int u)
 {
     int lo = 0, hi = E - 1;
     while (lo < hi) {
@@ -124,6 +177,10 @@ __device__ __forceinline__ int find_expert(const Plan &pl, int E, int u)
     }
     return lo;
 }
+
+// Worker w of n takes units w, 2n-1-w, 2n+w, 4n-1-w, ...: with units that get shorter, what a worker gains in one
+// round it gives back in the next. The unit of round i, which may be past the last one.
+__device__ __forceinline__ int unit_of(int i, int w, int n) { return i * n + ((i & 1) ? n - 1 - w : w); }
 
 __device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b, int type)
 {
@@ -135,20 +192,19 @@ __device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b, int type)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Lane = feature, v[j] = token j: stores up to `n` tokens' rows. Neighbour lanes trade halves, so a lane stores two
-// features of one token: even lanes the even tokens, odd lanes the odd ones (64 bytes of a row a warp).
+// Lane = feature, w[j] = tokens 2j and 2j + 1, packed: stores up to `n` tokens' rows. Neighbour lanes trade halves, so a
+// lane stores two features of one token: even lanes the even tokens, odd lanes the odd ones (64 bytes of a row a warp).
 template <int COLS>
-__device__ __forceinline__ void store_tokens(const uint32_t (&v)[COLS], uint16_t *out, int64_t ld, int f, int M, int n,
-                                             int type)
+__device__ __forceinline__ void store_tokens(const uint32_t (&w)[COLS / 2], uint16_t *out, int64_t ld, int f, int M, int n)
 {
     const bool odd = f & 1;
 #pragma unroll
     for (int j = 0; j < COLS; j += 2) {
-        const uint32_t mine = pack2(v[j], v[j + 1], type);
+        const uint32_t mine = w[j / 2];
         const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-        const uint32_t w = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+        const uint32_t both = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
         const int t = j + odd;
-        if (t < n && f < M) *reinterpret_cast<uint32_t *>(out + (int64_t)t * ld + (f & ~1)) = w;
+        if (t < n && f < M) *reinterpret_cast<uint32_t *>(out + (int64_t)t * ld + (f & ~1)) = both;
     }
 }
 
@@ -158,26 +214,75 @@ __device__ __forceinline__ void store_tokens(const uint32_t (&v)[COLS], uint16_t
 
 struct PUnit {
     int e, m0, t0, n;          // expert, first accumulator row, first token, tokens
+    int n0, n1;                // accumulator columns of the two halves (steps of 32; n1 may be 0)
 };
 
 __device__ __forceinline__ PUnit pair_unit(const Plan &pl, const GArgs &g, int u)
 {
     PUnit x;
-    x.e = find_expert(pl, g.E, u);
+    const int place = find_place(pl, g.E, u);
+    x.e = pl.order[place];
     const int cnt = pl.off[x.e + 1] - pl.off[x.e];
-    const int tile = tile_tokens(cnt, PN, 32), tiles = (cnt + tile - 1) / tile;
+    const int tile = tile_tokens(cnt, pl.most, 32), tiles = (cnt + tile - 1) / tile;
     const int m_tiles = (g.M + PM - 1) / PM;
-    const int local = u - pl.pre[x.e];
-    // token tiles in bands of P_BAND, all weight tiles of a band before the next band: pairs at work together
+    const int local = u - pl.pre[place];
+    // token tiles in bands of T_BAND, all weight tiles of a band before the next band: pairs at work together
     // share weight tiles and a band's tokens in L2
-    const int band = local / (m_tiles * P_BAND);
-    const int in = local - band * m_tiles * P_BAND;
-    const int width = min(P_BAND, tiles - band * P_BAND);
-    const int mt = in / width, nt = band * P_BAND + in - mt * width;
+    const int band = local / (m_tiles * T_BAND);
+    const int in = local - band * m_tiles * T_BAND;
+    const int width = min(T_BAND, tiles - band * T_BAND);
+    const int mt = in / width, nt = band * T_BAND + in - mt * width;
     x.m0 = mt * PM;
     x.t0 = pl.off[x.e] + nt * tile;
     x.n = min(tile, cnt - nt * tile);
+    x.n0 = min((x.n + 31) & ~31, PN);
+    x.n1 = ((x.n + 31) & ~31) - x.n0;
     return x;
+}
+
+// The tile size for these offsets: the one whose rounds of units, at the mean cost of a unit, end first. A unit's time
+// is about that of its accumulator columns and 128 more, for its weights and its ends (measured, 4 rounds of 4,096-long
+// sums: 154, 204 and 248 us at 256, 384 and 512 tokens), so large tiles win unless they leave the last round empty.
+__device__ __forceinline__ void choose_tile(Plan &pl, const GArgs &g, int workers)
+{
+    if (threadIdx.x < kCands) pl.cand_units[threadIdx.x] = pl.cand_cost[threadIdx.x] = 0;
+    __syncthreads();
+    const int m_tiles = (g.M + PM - 1) / PM;
+    for (int base = 0; base < g.E; base += blockDim.x) {
+        const int e = base + threadIdx.x;
+        const int cnt = e < g.E ? pl.off[e + 1] - pl.off[e] : 0;
+        for (int i = 0; i < kCands; ++i) {
+            int tiles = 0, cost = 0;
+            if (cnt > 0) {
+                const int tile = tile_tokens(cnt, cand_tokens(i), 32);
+                tiles = (cnt + tile - 1) / tile;
+                const int last = cnt - (tiles - 1) * tile;
+                cost = (tiles - 1) * (tile + 128) + ((last + 31) & ~31) + 128;
+            }
+            tiles = __reduce_add_sync(0xffffffffu, tiles);
+            cost = __reduce_add_sync(0xffffffffu, cost);
+            if ((threadIdx.x & 31) == 0 && tiles) {
+                atomicAdd(&pl.cand_units[i], tiles);
+                atomicAdd(&pl.cand_cost[i], cost);
+            }
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float best = 0.0f;
+        pl.most = T_TOKENS;
+        for (int i = 0; i < kCands; ++i) {
+            const float tiles = (float)pl.cand_units[i];
+            if (tiles == 0.0f) break;
+            const float rounds = ceilf(tiles * (float)m_tiles / (float)workers);
+            const float t = rounds * (float)pl.cand_cost[i] / tiles;
+            if (i == 0 || t < best) {
+                best = t;
+                pl.most = cand_tokens(i);
+            }
+        }
+    }
+    __syncthreads();
 }
 
 template <bool TRANS>
@@ -185,7 +290,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full_bar[P_STAGES], empty_bar[P_STAGES], tfull_bar[P_NBUF], tempty_bar[P_NBUF], drain_bar;
+    __shared__ uint64_t full_bar[T_STAGES], empty_bar[T_STAGES], tfull_bar[2], tempty_bar[2], drain_bar;
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile int abort_flag;
     __shared__ Plan pl;
@@ -194,15 +299,15 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t crank = cluster_ctarank();
     const bool leader = crank == 0;
-    const int unit0 = blockIdx.x / 2, ustep = gridDim.x / 2;
+    const int worker = blockIdx.x / 2, workers = gridDim.x / 2;
 
     if (tid == 0) {
         abort_flag = 0;
-        for (int s = 0; s < P_STAGES; ++s) {
+        for (int s = 0; s < T_STAGES; ++s) {
             mbar_init(&full_bar[s], 1);
             mbar_init(&empty_bar[s], 1);
         }
-        for (int a = 0; a < P_NBUF; ++a) {
+        for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull_bar[a], 1);
             mbar_init(&tempty_bar[a], P_EPI_WARPS * 2);
         }
@@ -211,16 +316,17 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         prefetch_tmap(&g.tm_w);
         prefetch_tmap(&g.tm_x);
     }
-    const int m_tiles = (g.M + PM - 1) / PM;
-    const bool valid = load_plan(pl, g.offsets, g.E, g.T, [&](int cnt) {
-        if (cnt == 0) return 0;
-        const int tile = tile_tokens(cnt, PN, 32);
-        return (cnt + tile - 1) / tile * m_tiles;
-    });
-    if (!valid) {                                 // both CTAs of every pair see the same offsets
+    if (!load_offsets(pl, g.offsets, g.E, g.T)) {     // both CTAs of every pair see the same offsets
         if (blockIdx.x == 0 && tid == 0) set_status(status, SF_STATUS_BAD_OFFSET);
         return;
     }
+    choose_tile(pl, g, workers);
+    order_experts(pl, g.E, [&](int cnt) { return cnt > 0 ? tile_tokens(cnt, pl.most, 32) : 0; });
+    count_units(pl, g.E, [&](int cnt) {
+        if (cnt == 0) return 0;
+        const int tile = tile_tokens(cnt, pl.most, 32);
+        return (cnt + tile - 1) / tile * ((g.M + PM - 1) / PM);
+    });
     if (warp == 1) tmem_alloc_pair(&tmem_base_s, P_TMEM_COLS);
     tc_fence_before();
     __syncthreads();
@@ -235,27 +341,31 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            bool issued[P_STAGES] = {};
-            uint32_t issued_parity[P_STAGES] = {};
+            bool issued[T_STAGES] = {};
+            uint32_t issued_parity[T_STAGES] = {};
             bool ok = true;
-            for (int u = unit0; u < total_units && ok; u += ustep) {
+            for (int i = 0; i * workers < total_units && ok; ++i) {
+                const int u = unit_of(i, worker, workers);
+                if (u >= total_units) break;
                 const PUnit x = pair_unit(pl, g, u);
-                const int half_n = ((x.n + 31) & ~31) / 2;
-                const int m = x.m0 + (int)crank * 128, t = x.t0 + (int)crank * half_n;
+                const int m = x.m0 + (int)crank * 128;
+                const int ta = x.t0 + (int)crank * (x.n0 / 2), tb = x.t0 + x.n0 + (int)crank * (x.n1 / 2);
+                const uint32_t bytes = 2 * (uint32_t)P_HALF_BYTES * (x.n1 ? 3 : 2);
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag)) { ok = false; break; }
-                    uint8_t *sw = smem + stage * P_STAGE_BYTES, *sx = sw + P_HALF_BYTES;
-                    if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * P_STAGE_BYTES);
+                    uint8_t *sw = smem + stage * T_STAGE_BYTES, *sx = sw + P_HALF_BYTES;
+                    if (leader) mbar_arrive_expect_tx(&full_bar[stage], bytes);
                     if (TRANS) {
                         tma_load_3d_pair(sw, &g.tm_w, &full_bar[stage], m, kb * GK, x.e);
                         tma_load_3d_pair(sw + G_BOX_BYTES, &g.tm_w, &full_bar[stage], m + 64, kb * GK, x.e);
                     } else {
                         tma_load_3d_pair(sw, &g.tm_w, &full_bar[stage], kb * GK, m, x.e);
                     }
-                    tma_load_2d_pair(sx, &g.tm_x, &full_bar[stage], kb * GK, t);
+                    tma_load_2d_pair(sx, &g.tm_x, &full_bar[stage], kb * GK, ta);
+                    if (x.n1) tma_load_2d_pair(sx + P_HALF_BYTES, &g.tm_x, &full_bar[stage], kb * GK, tb);
                     issued[stage] = true;
                     issued_parity[stage] = phase;
-                    if (++stage == P_STAGES) { stage = 0; phase ^= 1u; }
+                    if (++stage == T_STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
             {   // the MMA issuer commits drain_bar once it has finished or given up
@@ -263,7 +373,7 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                 while (!mbar_try_wait(&drain_bar, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
             }
             if ((!ok || abort_flag) && leader) {  // both CTAs' loads complete on the leader's barriers
-                for (int s = 0; s < P_STAGES; ++s) {
+                for (int s = 0; s < T_STAGES; ++s) {
                     if (!issued[s]) continue;
                     const uint64_t t0 = globaltimer_ns();
                     while (!mbar_try_wait(&full_bar[s], issued_parity[s]) && globaltimer_ns() - t0 < kWaitLimitNs) {}
@@ -272,63 +382,128 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
-        if (lane == 0 && leader) {
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, buf_phase = 0;
+        if (leader) {
+            int stage = 0;
+            uint32_t phase = 0, half_phase = 0;   // half_phase: a bit a half, flipped by each use of it
             bool ok = true;
-            for (int u = unit0; u < total_units && ok; u += ustep) {
-                const PUnit x = pair_unit(pl, g, u);
-                const uint32_t id = idesc(g.type, TRANS, false, (x.n + 31) & ~31, PM);
-                const uint32_t d_tmem = tmem_base + (uint32_t)(buf * PN);
-                if (!mbar_wait(&tempty_bar[buf], buf_phase ^ 1u, &abort_flag)) break;
-                tc_fence_after();
-                for (int kb = 0; kb < nk; ++kb) {
-                    if (!mbar_wait(&full_bar[stage], phase, &abort_flag)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t sw = smem_u32(smem + stage * P_STAGE_BYTES), sx = sw + P_HALF_BYTES;
+            const uint32_t s0 = smem_u32(smem);
+            const uint64_t w0 = TRANS ? mnmajor(s0) : kmajor(s0), x0 = kmajor(s0 + P_HALF_BYTES);
+            // one half's MMAs of a stage: 16 of K are 32 bytes of a K-major row, or 16 rows of 128 bytes
+            auto half_stage = [&](int h, int st, uint32_t id, bool first, bool last, bool release) {
+                const uint64_t dw = w0 + (uint64_t)(st * (T_STAGE_BYTES >> 4));
+                const uint64_t dx = x0 + (uint64_t)(st * (T_STAGE_BYTES >> 4) + h * (P_HALF_BYTES >> 4));
+                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < GK / G_UMMA_K; ++k)       // 16 of K: 32 bytes of a row, or 16 rows
-                        mma_bf16_pair(d_tmem, TRANS ? mnmajor(sw + k * G_UMMA_K * 128) : kmajor(sw + k * 32),
-                                      kmajor(sx + k * 32), id, (kb | k) != 0);
-                    mma_commit_pair(&empty_bar[stage], 3);
-                    if (++stage == P_STAGES) { stage = 0; phase ^= 1u; }
+                    for (int k = 0; k < GK / G_UMMA_K; ++k)
+                        mma_bf16_pair(tmem_base + h * PN, dw + k * (TRANS ? 128 : 2), dx + k * 2, id, !first || k != 0);
+                    if (last) mma_commit_pair(&tfull_bar[h], 3);
+                    if (release) mma_commit_pair(&empty_bar[st], 3);
                 }
+                __syncwarp();
+            };
+            for (int i = 0; i * workers < total_units && ok; ++i) {
+                const int u = unit_of(i, worker, workers);
+                if (u >= total_units) break;
+                const PUnit x = pair_unit(pl, g, u);
+                const uint32_t id0 = idesc(g.type, TRANS, false, x.n0, PM), id1 = idesc(g.type, TRANS, false, x.n1, PM);
+                ok = __all_sync(0xffffffffu, mbar_wait(&tempty_bar[0], (half_phase & 1u) ^ 1u, &abort_flag));
                 if (!ok) break;
-                mma_commit_pair(&tfull_bar[buf], 3);
-                if (++buf == P_NBUF) { buf = 0; buf_phase ^= 1u; }
+                // The first stages of a unit run their first half alone, and then their second: that gives the epilogue
+                // the time of T_AHEAD half stages to drain the second half of the unit before.
+                const int ahead = x.n1 ? min(T_AHEAD, nk) : 0;
+                int kb = 0;
+                for (; kb < ahead && ok; ++kb) {
+                    const int st = stage + kb < T_STAGES ? stage + kb : stage + kb - T_STAGES;
+                    const uint32_t ph = stage + kb < T_STAGES ? phase : phase ^ 1u;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[st], ph, &abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+                    half_stage(0, st, id0, kb == 0, kb == nk - 1, false);
+                }
+                if (ok && ahead) ok = __all_sync(0xffffffffu, mbar_wait(&tempty_bar[1], (half_phase >> 1) ^ 1u, &abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                for (kb = 0; kb < ahead; ++kb) {
+                    half_stage(1, stage, id1, kb == 0, kb == nk - 1, true);
+                    if (++stage == T_STAGES) { stage = 0; phase ^= 1u; }
+                }
+                for (; kb < nk; ++kb) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, &abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+                    half_stage(0, stage, id0, kb == 0, kb == nk - 1, x.n1 == 0);
+                    if (x.n1) half_stage(1, stage, id1, false, kb == nk - 1, true);
+                    if (++stage == T_STAGES) { stage = 0; phase ^= 1u; }
+                }
+                half_phase ^= x.n1 ? 3u : 1u;
             }
-            mma_commit_pair(&drain_bar, 3);
+            if (elect_one()) mma_commit_pair(&drain_bar, 3);
+            __syncwarp();
             const uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(&drain_bar, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
         }
     } else {
         // --------------------------- epilogue (warps 2..9) ---------------------------
         const int quad = warp & 3;              // TMEM lanes 32*quad .. 32*quad+31
-        const int half = (warp - 2) >> 2;       // 32-token chunks half, half + 2, ...
-        int buf = 0;
-        uint32_t buf_phase = 0;
-        for (int u = unit0; u < total_units; u += ustep) {
+        const int part = (warp - 2) >> 2;       // 128 of a half's columns
+        uint8_t *s_out = smem + T_STAGES * T_STAGE_BYTES + part * T_OUT_BYTES;
+        uint32_t half_phase = 0;
+        bool ready = true;
+        for (int i = 0; i * workers < total_units && ready; ++i) {
+            const int u = unit_of(i, worker, workers);
+            if (u >= total_units) break;
             const PUnit x = pair_unit(pl, g, u);
-            const int f = x.m0 + (int)crank * 128 + quad * 32 + lane;
-            const bool ready = __all_sync(0xffffffffu, mbar_wait(&tfull_bar[buf], buf_phase, &abort_flag));
-            if (!ready) break;
-            tc_fence_after();
-            const uint32_t t_row = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * PN);
-            for (int c = half * 32; c < x.n; c += 64) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(t_row + c, v);
-                tmem_ld_wait();
-                store_tokens<32>(v, static_cast<uint16_t *>(g.out) + (int64_t)(x.t0 + c) * g.ld_out, g.ld_out, f, g.M,
-                                 x.n - c, g.type);
+            const int m = x.m0 + (int)crank * 128, bytes = 2 * min(128, g.M - m);
+            for (int h = 0; h < (x.n1 ? 2 : 1); ++h) {
+                ready = mbar_wait(&tfull_bar[h], half_phase >> h & 1u, &abort_flag);
+                ready = bar_all(1 + part, 128, ready);       // the part's warps go on together or not at all
+                if (!ready) break;
+                tc_fence_after();
+                // all of this warp's columns, packed, into registers, so that the MMAs get the accumulator back at once
+                const int c0 = part * 128, cols = (h ? x.n1 : x.n0) - c0;
+                const uint32_t t_row = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(h * PN + c0);
+                uint32_t w[4][16];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (q * 32 < cols) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(t_row + q * 32, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[q][j] = pack2(v[2 * j], v[2 * j + 1], g.type);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader) mbar_arrive(&tempty_bar[h]);
+                    else mbar_arrive_remote(&tempty_bar[h], 0);
+                }
+                // Out through shared memory, 32 tokens at a time: the part's four warps lay down each token's 128
+                // features, 64 bytes a warp, and a lane sends each token's row as one bulk copy.
+                const int t0 = h * PN + c0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (q * 32 >= cols) break;
+                    bulk_wait_read<0>();
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
+                    uint16_t *slot = reinterpret_cast<uint16_t *>(s_out) + quad * 32 + lane;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        slot[(2 * j) * 128] = (uint16_t)w[q][j];
+                        slot[(2 * j + 1) * 128] = (uint16_t)(w[q][j] >> 16);
+                    }
+                    fence_proxy_async_smem();
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
+                    const int row = quad * 8 + lane, t = t0 + q * 32 + row;
+                    if (lane < 8 && t < x.n && bytes > 0)
+                        bulk_store(static_cast<uint16_t *>(g.out) + (int64_t)(x.t0 + t) * g.ld_out + m, s_out + row * 256, bytes);
+                    bulk_commit();
+                }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (leader) mbar_arrive(&tempty_bar[buf]);
-                else mbar_arrive_remote(&tempty_bar[buf], 0);
-            }
-            if (++buf == P_NBUF) { buf = 0; buf_phase ^= 1u; }
+            half_phase ^= x.n1 ? 3u : 1u;
         }
+        bulk_wait_all();
     }
 
     __syncwarp();
@@ -363,15 +538,17 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
     const int u = blockIdx.x / ks;
 
     const int m_tiles = (g.M + SM_ROWS - 1) / SM_ROWS;
-    const bool valid = load_plan(pl, g.offsets, g.E, g.T, [&](int cnt) {
+    if (!load_offsets(pl, g.offsets, g.E, g.T)) {
+        if (blockIdx.x == 0 && tid == 0) set_status(status, SF_STATUS_BAD_OFFSET);
+        return;
+    }
+    for (int e = tid; e < g.E; e += blockDim.x) pl.order[e] = (uint16_t)e;
+    __syncthreads();
+    count_units(pl, g.E, [&](int cnt) {
         if (cnt == 0) return 0;
         const int tile = tile_tokens(cnt, nb, 16);
         return (cnt + tile - 1) / tile * m_tiles;
     });
-    if (!valid) {
-        if (blockIdx.x == 0 && tid == 0) set_status(status, SF_STATUS_BAD_OFFSET);
-        return;
-    }
     if (u >= pl.pre[g.E]) return;               // the whole cluster
     if (tid == 0) {
         abort_flag = 0;
@@ -391,7 +568,7 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
     tc_fence_after();
     const uint32_t tmem_base = tmem_base_s;
 
-    const int e = find_expert(pl, g.E, u);
+    const int e = find_place(pl, g.E, u);
     const int cnt = pl.off[e + 1] - pl.off[e];
     const int tile = tile_tokens(cnt, nb, 16), tiles = (cnt + tile - 1) / tile;
     const int local = u - pl.pre[e], mt = local / tiles, nt = local - mt * tiles;     // tiles of one weight tile adjoin
@@ -430,23 +607,27 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            const uint32_t id = idesc(g.type, TRANS, false, (n + 15) & ~15, SM_ROWS);
-            for (int i = 0; i < nk; ++i) {
-                if (!mbar_wait(&full_bar[stage], phase, &abort_flag)) break;
-                tc_fence_after();
-                const uint32_t sw = smem_u32(smem + stage * stage_bytes), sx = sw + S_W_BYTES;
+        int stage = 0;
+        uint32_t phase = 0;
+        const uint32_t id = idesc(g.type, TRANS, false, (n + 15) & ~15, SM_ROWS);
+        const uint32_t s0 = smem_u32(smem);
+        const uint64_t w0 = TRANS ? mnmajor(s0) : kmajor(s0), x0 = kmajor(s0 + S_W_BYTES);
+        int i = 0;
+        for (; i < nk; ++i) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, &abort_flag))) break;
+            tc_fence_after();
+            const uint64_t dw = w0 + (uint64_t)(stage * (stage_bytes >> 4)), dx = x0 + (uint64_t)(stage * (stage_bytes >> 4));
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < GK / G_UMMA_K; ++k)
-                    mma_bf16(tmem_base, TRANS ? mnmajor(sw + k * G_UMMA_K * 128) : kmajor(sw + k * 32), kmajor(sx + k * 32),
-                             id, (i | k) != 0);
+                    mma_bf16(tmem_base, dw + k * (TRANS ? 128 : 2), dx + k * 2, id, (i | k) != 0);
                 mma_commit(&empty_bar[stage]);
-                if (++stage == stages) { stage = 0; phase ^= 1u; }
+                if (i == nk - 1) mma_commit(&done_bar);
             }
-            mma_commit(&done_bar);
+            __syncwarp();
+            if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
+        if (i < nk && elect_one()) mma_commit(&done_bar);     // gave up
     }
     __syncwarp();
     // Everyone waits for the MMAs (the producer has, in lane 0); a CTA that gave up tells its cluster.
@@ -460,10 +641,12 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
     if (ks == 1) {
         if (warp >= 2 && !abort_flag) {
             for (int c = 0; c < n; c += 16) {
-                uint32_t v[16];
+                uint32_t v[16], w[8];
                 tmem_ld_32x32b_x16(t_row + c, v);
                 tmem_ld_wait();
-                store_tokens<16>(v, out + (int64_t)c * g.ld_out, g.ld_out, f, g.M, n - c, g.type);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], g.type);
+                store_tokens<16>(w, out + (int64_t)c * g.ld_out, g.ld_out, f, g.M, n - c);
             }
         }
     } else {
@@ -511,48 +694,63 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 // ------------------------------------------------------------------------------------------------
 
 struct WUnit {
-    int e, r0, c0, t0, cnt;
+    int e, r0, c0, t0, cnt;    // expert, first row, first column, first token, tokens
+    int n0, n1;                // columns of the two halves (steps of 32; n1 may be 0)
+    int nk, chunks, per;       // stages of 64 tokens, accumulation chunks, stages to a chunk
 };
 
-__device__ __forceinline__ WUnit dw_unit(const Plan &pl, const GArgs &g, int u)
+// Experts in the order of their numbers, or of `order` (falling stage counts) where there is one.
+struct WPlan {
+    uint16_t order[kSortE];
+};
+
+__device__ __forceinline__ WUnit dw_unit(const WPlan &pl, const GArgs &g, int u)
 {
-    const int m_tiles = (g.M + PM - 1) / PM, n_tiles = (g.K + PN - 1) / PN;
-    const int per = m_tiles * n_tiles;
+    const int tile = tile_tokens(g.K, T_TOKENS, 64), n_tiles = (g.K + tile - 1) / tile;
+    const int m_tiles = (g.M + PM - 1) / PM, per = m_tiles * n_tiles;
     WUnit x;
-    x.e = u / per;
-    const int local = u - x.e * per, mt = local / n_tiles;
+    const int place = u / per, local = u - place * per, mt = local / n_tiles;
+    x.e = g.E <= kSortE ? pl.order[place] : place;
     x.r0 = mt * PM;
-    x.c0 = (local - mt * n_tiles) * PN;
-    x.t0 = pl.off[x.e];
-    x.cnt = pl.off[x.e + 1] - x.t0;
+    x.c0 = (local - mt * n_tiles) * tile;
+    const int n = (min(tile, g.K - x.c0) + 31) & ~31;
+    x.n0 = min(n, PN);
+    x.n1 = n - x.n0;
+    x.t0 = __ldg(g.offsets + x.e);
+    x.cnt = __ldg(g.offsets + x.e + 1) - x.t0;
+    x.nk = (x.cnt + GK - 1) / GK;
+    x.chunks = g.out_f32 ? (x.nk + W_CHUNK_STAGES - 1) / W_CHUNK_STAGES : min(x.nk, 1);
+    x.per = x.chunks ? (x.nk + x.chunks - 1) / x.chunks : 0;
     return x;
 }
 
-__global__ void __launch_bounds__(P_THREADS, 1)
+__device__ __forceinline__ bool has_tail(const WUnit &x) { return (x.cnt & (G_UMMA_K - 1)) != 0; }
+
+__global__ void __launch_bounds__(W_THREADS, 1)
 grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full_bar[P_STAGES], empty_bar[P_STAGES], tfull_bar[P_NBUF], tempty_bar[P_NBUF], drain_bar;
-    __shared__ uint64_t tail_bar[P_STAGES], clear_bar[P_STAGES];   // for the last stage of an expert, where rows are cleared
+    __shared__ uint64_t full_bar[T_STAGES], empty_bar[T_STAGES], tfull_bar[2], tempty_bar[2], drain_bar;
+    __shared__ uint64_t tail_bar[T_STAGES], clear_bar[T_STAGES];   // for the last stage of an expert, where rows are cleared
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile int abort_flag;
-    __shared__ Plan pl;
+    __shared__ WPlan pl;
 
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t crank = cluster_ctarank();
     const bool leader = crank == 0;
-    const int unit0 = blockIdx.x / 2, ustep = gridDim.x / 2;
+    const int worker = blockIdx.x / 2, workers = gridDim.x / 2;
 
     if (tid == 0) {
         abort_flag = 0;
-        for (int s = 0; s < P_STAGES; ++s) {
+        for (int s = 0; s < T_STAGES; ++s) {
             mbar_init(&full_bar[s], 1);
             mbar_init(&empty_bar[s], 1);
             mbar_init(&tail_bar[s], 1);           // this CTA's loads of the stage have landed
             mbar_init(&clear_bar[s], 2);          // the leader's: both CTAs have cleared their rows
         }
-        for (int a = 0; a < P_NBUF; ++a) {
+        for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull_bar[a], 1);
             mbar_init(&tempty_bar[a], P_EPI_WARPS * 2);
         }
@@ -560,11 +758,29 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         fence_mbarrier_init();
         prefetch_tmap(&g.tm_w);
         prefetch_tmap(&g.tm_x);
+        prefetch_tmap(&g.tm_out);
     }
-    const bool valid = load_plan(pl, g.offsets, g.E, g.T, [](int) { return 0; });
-    if (!valid) {
-        if (blockIdx.x == 0 && tid == 0) set_status(status, SF_STATUS_BAD_OFFSET);
-        return;
+    {   // offsets: valid, and the experts' order
+        int bad = 0;
+        int *keys = reinterpret_cast<int *>(smem);                  // before the stages are used
+        for (int e = tid; e < g.E; e += blockDim.x) {
+            const int o0 = g.offsets[e], o1 = g.offsets[e + 1];
+            if (o0 < 0 || o1 < o0 || o1 > g.T) bad = 1;
+            if (g.E <= kSortE) keys[e] = (o1 - o0 + GK - 1) / GK;
+        }
+        if (__syncthreads_or(bad)) {
+            if (blockIdx.x == 0 && tid == 0) set_status(status, SF_STATUS_BAD_OFFSET);
+            return;
+        }
+        if (g.E <= kSortE)
+            for (int e = tid; e < g.E; e += blockDim.x) {
+                const int mine = keys[e];
+                int rank = 0;
+                for (int k = 0; k < g.E; ++k) rank += keys[k] > mine || (keys[k] == mine && k < e);
+                pl.order[rank] = (uint16_t)e;
+            }
+        __syncthreads();
+        fence_proxy_async_smem();                                   // the stages are written by TMA from here on
     }
     if (warp == 1) tmem_alloc_pair(&tmem_base_s, P_TMEM_COLS);
     tc_fence_before();
@@ -572,45 +788,57 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = tmem_base_s;
-    const int total_units = g.E * ((g.M + PM - 1) / PM) * ((g.K + PN - 1) / PN);
+    const int tile_c = tile_tokens(g.K, T_TOKENS, 64);
+    const int total_units = g.E * ((g.M + PM - 1) / PM) * ((g.K + tile_c - 1) / tile_c);
 
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            bool issued[P_STAGES] = {};
-            uint32_t issued_parity[P_STAGES] = {};
+            bool issued[T_STAGES] = {};
+            uint32_t issued_parity[T_STAGES] = {};
             uint32_t tails = 0, tail_parity = 0;  // by stage: whether it held a tail, and the parity of its last one
             bool ok = true;
-            for (int u = unit0; u < total_units && ok; u += ustep) {
+            for (int i = 0; i * workers < total_units && ok; ++i) {
+                const int u = unit_of(i, worker, workers);
+                if (u >= total_units) break;
                 const WUnit x = dw_unit(pl, g, u);
-                const int nk = (x.cnt + GK - 1) / GK;
-                const int r = x.r0 + (int)crank * 128, c = x.c0 + (int)crank * 128;
-                for (int kb = 0; kb < nk; ++kb) {
+                const int r = x.r0 + (int)crank * 128;
+                const int ca = x.c0 + (int)crank * (x.n0 / 2), cb = x.c0 + x.n0 + (int)crank * (x.n1 / 2);
+                const uint32_t bytes = (uint32_t)P_HALF_BYTES * (x.n1 ? 3 : 2);
+                for (int kb = 0; kb < x.nk; ++kb) {
                     if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag)) { ok = false; break; }
-                    uint8_t *sy = smem + stage * P_STAGE_BYTES, *sa = sy + P_HALF_BYTES;
+                    uint8_t *sy = smem + stage * T_STAGE_BYTES, *sa = sy + P_HALF_BYTES, *sb = sa + P_HALF_BYTES;
                     const int t = x.t0 + kb * GK;
-                    if (kb == nk - 1 && (x.cnt & (G_UMMA_K - 1))) {
+                    if (kb == x.nk - 1 && has_tail(x)) {
                         // rows to clear: each CTA's loads complete on its own barrier, for the warp that clears them
                         if (leader) mbar_arrive(&full_bar[stage]);
-                        mbar_arrive_expect_tx(&tail_bar[stage], P_STAGE_BYTES);
+                        mbar_arrive_expect_tx(&tail_bar[stage], bytes);
                         tma_load_2d(sy, &g.tm_x, &tail_bar[stage], r, t);
                         tma_load_2d(sy + G_BOX_BYTES, &g.tm_x, &tail_bar[stage], r + 64, t);
-                        tma_load_2d(sa, &g.tm_w, &tail_bar[stage], c, t);
-                        tma_load_2d(sa + G_BOX_BYTES, &g.tm_w, &tail_bar[stage], c + 64, t);
+                        tma_load_2d(sa, &g.tm_w, &tail_bar[stage], ca, t);
+                        tma_load_2d(sa + G_BOX_BYTES, &g.tm_w, &tail_bar[stage], ca + 64, t);
+                        if (x.n1) {
+                            tma_load_2d(sb, &g.tm_w, &tail_bar[stage], cb, t);
+                            tma_load_2d(sb + G_BOX_BYTES, &g.tm_w, &tail_bar[stage], cb + 64, t);
+                        }
                         if (tails >> stage & 1u) tail_parity ^= 1u << stage;
                         tails |= 1u << stage;
                     } else {
-                        if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * P_STAGE_BYTES);
+                        if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * bytes);
                         tma_load_2d_pair(sy, &g.tm_x, &full_bar[stage], r, t);
                         tma_load_2d_pair(sy + G_BOX_BYTES, &g.tm_x, &full_bar[stage], r + 64, t);
-                        tma_load_2d_pair(sa, &g.tm_w, &full_bar[stage], c, t);
-                        tma_load_2d_pair(sa + G_BOX_BYTES, &g.tm_w, &full_bar[stage], c + 64, t);
+                        tma_load_2d_pair(sa, &g.tm_w, &full_bar[stage], ca, t);
+                        tma_load_2d_pair(sa + G_BOX_BYTES, &g.tm_w, &full_bar[stage], ca + 64, t);
+                        if (x.n1) {
+                            tma_load_2d_pair(sb, &g.tm_w, &full_bar[stage], cb, t);
+                            tma_load_2d_pair(sb + G_BOX_BYTES, &g.tm_w, &full_bar[stage], cb + 64, t);
+                        }
                     }
                     issued[stage] = true;
                     issued_parity[stage] = phase;
-                    if (++stage == P_STAGES) { stage = 0; phase ^= 1u; }
+                    if (++stage == T_STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
             {
@@ -619,13 +847,13 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
             }
             if (!ok || abort_flag) {
                 if (leader) {
-                    for (int s = 0; s < P_STAGES; ++s) {
+                    for (int s = 0; s < T_STAGES; ++s) {
                         if (!issued[s]) continue;
                         const uint64_t t0 = globaltimer_ns();
                         while (!mbar_try_wait(&full_bar[s], issued_parity[s]) && globaltimer_ns() - t0 < kWaitLimitNs) {}
                     }
                 }
-                for (int s = 0; s < P_STAGES; ++s) {
+                for (int s = 0; s < T_STAGES; ++s) {
                     if (!(tails >> s & 1u)) continue;
                     const uint64_t t0 = globaltimer_ns();
                     while (!mbar_try_wait(&tail_bar[s], tail_parity >> s & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {}
@@ -633,131 +861,212 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
             }
         }
     } else if (warp == 1) {
-        // ---------------- MMA issuer (leader); clearing of rows behind an expert's end (both) ----------------
-        int stage = 0, buf = 0;
-        uint32_t phase = 0, buf_phase = 0, tail_phase = 0;     // tail_phase: a bit a stage
-        bool ok = true;
-        for (int u = unit0; u < total_units && ok; u += ustep) {
-            const WUnit x = dw_unit(pl, g, u);
-            const int nk = (x.cnt + GK - 1) / GK;
-            const uint32_t id = idesc(g.type, true, true, PN, PM);
-            for (int kb = 0; kb < nk; ++kb) {
-                const int in_chunk = kb % W_CHUNK_STAGES;
-                const bool tail = kb == nk - 1 && (x.cnt & (G_UMMA_K - 1));
-                uint8_t *sy = smem + stage * P_STAGE_BYTES;
-                if (tail) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&tail_bar[stage], tail_phase >> stage & 1u, &abort_flag));
-                    if (!ok) break;
-                    const int from = x.cnt - kb * GK, upto = (from + G_UMMA_K - 1) & ~(G_UMMA_K - 1);
-                    // a token is one 128-byte row of each of the stage's four boxes
-                    for (int i = lane; i < (upto - from) * 8; i += 32)
+        // ------------------------------ MMA issuer ------------------------------
+        if (leader) {
+            int stage = 0;
+            uint32_t phase = 0, half_phase = 0, clear_phase = 0;   // a bit a half; a bit a stage
+            bool ok = true;
+            const uint32_t s0 = smem_u32(smem);
+            const uint64_t y0 = mnmajor(s0), a0 = mnmajor(s0 + P_HALF_BYTES);
+            auto half_stage = [&](int h, int st, uint32_t id, int steps, bool first, bool last, bool release) {
+                const uint64_t dy = y0 + (uint64_t)(st * (T_STAGE_BYTES >> 4));
+                const uint64_t da = a0 + (uint64_t)(st * (T_STAGE_BYTES >> 4) + h * (P_HALF_BYTES >> 4));
+                if (elect_one()) {
+                    if (steps == GK / G_UMMA_K) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            *reinterpret_cast<uint4 *>(sy + q * G_BOX_BYTES + (from + (i >> 3)) * 128 + (i & 7) * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (leader) mbar_arrive(&clear_bar[stage]);
-                        else mbar_arrive_remote(&clear_bar[stage], 0);
+                        for (int k = 0; k < GK / G_UMMA_K; ++k)
+                            mma_bf16_pair(tmem_base + h * PN, dy + k * 128, da + k * 128, id, !first || k != 0);
+                    } else {
+                        for (int k = 0; k < steps; ++k)
+                            mma_bf16_pair(tmem_base + h * PN, dy + k * 128, da + k * 128, id, !first || k != 0);
                     }
+                    if (last) mma_commit_pair(&tfull_bar[h], 3);
+                    if (release) mma_commit_pair(&empty_bar[st], 3);
                 }
-                if (leader) {
-                    if (lane == 0) {
-                        if (in_chunk == 0) ok = mbar_wait(&tempty_bar[buf], buf_phase ^ 1u, &abort_flag);
-                        if (ok) ok = mbar_wait(&full_bar[stage], phase, &abort_flag);
-                        if (ok && tail) ok = mbar_wait_cluster(&clear_bar[stage], tail_phase >> stage & 1u, &abort_flag);
-                        if (ok) {
-                            tc_fence_after();
-                            const uint32_t a = smem_u32(sy), bb = a + P_HALF_BYTES;
-                            const uint32_t d_tmem = tmem_base + (uint32_t)(buf * PN);
-                            const int steps = min(GK, x.cnt - kb * GK + G_UMMA_K - 1) / G_UMMA_K;
-                            for (int k = 0; k < steps; ++k)
-                                mma_bf16_pair(d_tmem, mnmajor(a + k * G_UMMA_K * 128), mnmajor(bb + k * G_UMMA_K * 128), id,
-                                              (in_chunk | k) != 0);
-                            mma_commit_pair(&empty_bar[stage], 3);
-                            if (in_chunk == W_CHUNK_STAGES - 1 || kb == nk - 1) mma_commit_pair(&tfull_bar[buf], 3);
-                        }
+                __syncwarp();
+            };
+            for (int i = 0; i * workers < total_units && ok; ++i) {
+                const int u = unit_of(i, worker, workers);
+                if (u >= total_units) break;
+                const WUnit x = dw_unit(pl, g, u);
+                const uint32_t id0 = idesc(g.type, true, true, x.n0, PM), id1 = idesc(g.type, true, true, x.n1, PM);
+                const int rest = x.cnt - (x.nk - 1) * GK;               // tokens of the last stage
+                auto steps_of = [&](int kb) { return kb == x.nk - 1 ? (rest + G_UMMA_K - 1) / G_UMMA_K : GK / G_UMMA_K; };
+                // Waits for stage kb in slot st; the last one also for the cleared rows.
+                auto arrived = [&](int kb, int st, uint32_t ph) {
+                    bool there = mbar_wait(&full_bar[st], ph, &abort_flag);
+                    if (there && kb == x.nk - 1 && has_tail(x)) {
+                        there = mbar_wait_cluster(&clear_bar[st], clear_phase >> st & 1u, &abort_flag);
+                        clear_phase ^= 1u << st;
                     }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    return __all_sync(0xffffffffu, there) != 0;
+                };
+                for (int ch = 0; ch < x.chunks && ok; ++ch) {
+                    const int begin = ch * x.per, end = min(x.nk, begin + x.per);
+                    ok = __all_sync(0xffffffffu, mbar_wait(&tempty_bar[0], (half_phase & 1u) ^ 1u, &abort_flag));
                     if (!ok) break;
-                    if (in_chunk == W_CHUNK_STAGES - 1 || kb == nk - 1)
-                        if (++buf == P_NBUF) { buf = 0; buf_phase ^= 1u; }
+                    // as in the forward kernel: first halves of the first stages, then their second halves
+                    const int ahead = x.n1 ? begin + min(T_AHEAD, end - begin) : begin;
+                    int kb = begin;
+                    for (; kb < ahead && ok; ++kb) {
+                        const int at = stage + kb - begin, st = at < T_STAGES ? at : at - T_STAGES;
+                        ok = arrived(kb, st, at < T_STAGES ? phase : phase ^ 1u);
+                        if (!ok) break;
+                        tc_fence_after();
+                        half_stage(0, st, id0, steps_of(kb), kb == begin, kb == end - 1, false);
+                    }
+                    if (ok && x.n1) ok = __all_sync(0xffffffffu, mbar_wait(&tempty_bar[1], (half_phase >> 1) ^ 1u, &abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+                    for (kb = begin; kb < ahead; ++kb) {
+                        half_stage(1, stage, id1, steps_of(kb), kb == begin, kb == end - 1, true);
+                        if (++stage == T_STAGES) { stage = 0; phase ^= 1u; }
+                    }
+                    for (; kb < end; ++kb) {
+                        ok = arrived(kb, stage, phase);
+                        if (!ok) break;
+                        tc_fence_after();
+                        half_stage(0, stage, id0, steps_of(kb), kb == begin, kb == end - 1, x.n1 == 0);
+                        if (x.n1) half_stage(1, stage, id1, steps_of(kb), false, kb == end - 1, true);
+                        if (++stage == T_STAGES) { stage = 0; phase ^= 1u; }
+                    }
+                    half_phase ^= x.n1 ? 3u : 1u;
                 }
-                if (tail) tail_phase ^= 1u << stage;
-                if (++stage == P_STAGES) { stage = 0; phase ^= 1u; }
             }
-        }
-        if (leader && lane == 0) {
-            mma_commit_pair(&drain_bar, 3);
+            if (elect_one()) mma_commit_pair(&drain_bar, 3);
+            __syncwarp();
             const uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(&drain_bar, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+        }
+    } else if (warp == 2 + P_EPI_WARPS) {
+        // ---------------- clears the rows behind an expert's end, in this CTA's part of the stage ----------------
+        int stage = 0;
+        uint32_t tail_phase = 0;                // a bit a stage
+        for (int i = 0; i * workers < total_units; ++i) {
+            const int u = unit_of(i, worker, workers);
+            if (u >= total_units) break;
+            const WUnit x = dw_unit(pl, g, u);
+            if (has_tail(x)) {
+                const int st = (stage + x.nk - 1) % T_STAGES;
+                if (!__all_sync(0xffffffffu, mbar_wait(&tail_bar[st], tail_phase >> st & 1u, &abort_flag))) break;
+                tail_phase ^= 1u << st;
+                const int from = x.cnt - (x.nk - 1) * GK, upto = (from + G_UMMA_K - 1) & ~(G_UMMA_K - 1);
+                uint8_t *sy = smem + st * T_STAGE_BYTES;
+                // a token is one 128-byte row of each of the stage's boxes
+                for (int j = lane; j < (upto - from) * 8; j += 32)
+#pragma unroll
+                    for (int q = 0; q < T_STAGE_BYTES / G_BOX_BYTES; ++q)
+                        *reinterpret_cast<uint4 *>(sy + q * G_BOX_BYTES + (from + (j >> 3)) * 128 + (j & 7) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader) mbar_arrive(&clear_bar[st]);
+                    else mbar_arrive_remote(&clear_bar[st], 0);
+                }
+            }
+            stage = (stage + x.nk) % T_STAGES;
         }
     } else {
         // --------------------------- epilogue (warps 2..9) ---------------------------
         const int quad = warp & 3;              // accumulator rows 32*quad .. 32*quad+31 of the CTA
-        const int half = (warp - 2) >> 2;       // columns half*128 .. +127
-        int buf = 0;
-        uint32_t buf_phase = 0;
-        for (int u = unit0; u < total_units; u += ustep) {
+        const int part = (warp - 2) >> 2;       // 128 of a half's columns
+        uint8_t *s_out = smem + T_STAGES * T_STAGE_BYTES + (warp - 2) * W_OUT_BYTES;
+        uint4 *slot = reinterpret_cast<uint4 *>(s_out) + lane * 8;
+        uint32_t half_phase = 0;
+        bool ready = true;
+        for (int i = 0; i * workers < total_units && ready; ++i) {
+            const int u = unit_of(i, worker, workers);
+            if (u >= total_units) break;
             const WUnit x = dw_unit(pl, g, u);
-            const int nk = (x.cnt + GK - 1) / GK;
-            if (nk == 0 && g.accumulate) continue;
-            const int r = x.r0 + (int)crank * 128 + quad * 32 + lane, c0 = x.c0 + half * 128;
-            float acc[128];
-#pragma unroll
-            for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
-            bool ready = true;
-            const int nchunks = (nk + W_CHUNK_STAGES - 1) / W_CHUNK_STAGES;
-            for (int ch = 0; ch < nchunks; ++ch) {
-                ready = __all_sync(0xffffffffu, mbar_wait(&tfull_bar[buf], buf_phase, &abort_flag));
-                if (!ready) break;
-                tc_fence_after();
-                const uint32_t t_row = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * PN + half * 128);
-#pragma unroll
-                for (int cc = 0; cc < 4; ++cc) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(t_row + cc * 32, v);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[cc * 32 + j] = __fadd_rn(acc[cc * 32 + j], __uint_as_float(v[j]));
-                }
-                tc_fence_before();
+            const int row0 = x.r0 + (int)crank * 128 + quad * 32;
+            if (x.chunks == 0) {                // an expert without tokens
+                if (g.accumulate || row0 >= g.M) continue;
+                if (lane == 0) bulk_wait_read<0>();
                 __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) slot[j] = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                const int box = g.out_f32 ? 32 : 64;
                 if (lane == 0) {
-                    if (leader) mbar_arrive(&tempty_bar[buf]);
-                    else mbar_arrive_remote(&tempty_bar[buf], 0);
-                }
-                if (++buf == P_NBUF) { buf = 0; buf_phase ^= 1u; }
-            }
-            if (!ready) break;
-            if (r >= g.M) continue;
-            const int64_t at = (int64_t)x.e * g.stride_out + (int64_t)r * g.ld_out + c0;
-            if (g.out_f32) {
-                float *out = static_cast<float *>(g.out) + at;
-#pragma unroll
-                for (int j = 0; j < 128; j += 4) {
-                    if (c0 + j >= g.K) break;
-                    float4 v = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-                    if (g.accumulate) {
-                        const float4 o = *reinterpret_cast<const float4 *>(out + j);
-                        v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+                    for (int c = x.c0 + part * 128; c < min(x.c0 + x.n0 + x.n1, g.K); c += box) {
+                        if (((c - x.c0) & 128) != part * 128) continue;
+                        tma_store_3d(&g.tm_out, s_out, c, row0, x.e);
                     }
-                    *reinterpret_cast<float4 *>(out + j) = v;
+                    bulk_commit();
                 }
-            } else {
-                uint16_t *out = static_cast<uint16_t *>(g.out) + at;
+                continue;
+            }
+            for (int ch = 0; ch < x.chunks && ready; ++ch) {
+                const bool add = g.accumulate || ch > 0;
+                for (int h = 0; h < (x.n1 ? 2 : 1); ++h) {
+                    ready = __all_sync(0xffffffffu, mbar_wait(&tfull_bar[h], half_phase >> h & 1u, &abort_flag));
+                    if (!ready) break;
+                    tc_fence_after();
+                    // all of this warp's columns into registers, so that the MMAs get the accumulator back at once
+                    // (columns behind the half's last hold what an earlier tile left, and are not stored)
+                    const uint32_t t_row = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(h * PN + part * 128);
+                    uint32_t v[4][32];
 #pragma unroll
-                for (int j = 0; j < 128; j += 8) {
-                    if (c0 + j >= g.K) break;
-                    uint32_t w[4];
+                    for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(t_row + q * 32, v[q]);
+                    tmem_ld_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (leader) mbar_arrive(&tempty_bar[h]);
+                        else mbar_arrive_remote(&tempty_bar[h], 0);
+                    }
+                    const int c0 = x.c0 + h * PN + part * 128;
+                    const int cols = row0 < g.M ? min((h ? x.n1 : x.n0) - part * 128, g.K - c0) : 0;
+                    // A later chunk is added to what the chunk before left: that has to be there.
+                    if (ch > 0 && h == 0 && lane == 0) bulk_wait_all();
+                    // Out through shared memory, a box of 32 rows x 128 bytes at a time (16-byte units swizzled by
+                    // row, as the tensor map has it): what lies outside W the store leaves out.
+                    if (g.out_f32) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        w[q] = pack2(__float_as_uint(acc[j + 2 * q]), __float_as_uint(acc[j + 2 * q + 1]), g.type);
-                    *reinterpret_cast<uint4 *>(out + j) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int q = 0; q < 4; ++q) {
+                            if (q * 32 >= cols) break;
+                            if (lane == 0) bulk_wait_read<0>();
+                            __syncwarp();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                slot[j ^ (lane & 7)] = make_uint4(v[q][4 * j], v[q][4 * j + 1], v[q][4 * j + 2], v[q][4 * j + 3]);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (add) tma_add_3d(&g.tm_out, s_out, c0 + q * 32, row0, x.e);
+                                else tma_store_3d(&g.tm_out, s_out, c0 + q * 32, row0, x.e);
+                                bulk_commit();
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            if (q * 64 >= cols) break;
+                            if (lane == 0) bulk_wait_read<0>();
+                            __syncwarp();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    w[k] = pack2(v[2 * q + j / 4][8 * (j & 3) + 2 * k], v[2 * q + j / 4][8 * (j & 3) + 2 * k + 1], g.type);
+                                slot[j ^ (lane & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_store_3d(&g.tm_out, s_out, c0 + q * 64, row0, x.e);
+                                bulk_commit();
+                            }
+                        }
+                    }
                 }
+                half_phase ^= x.n1 ? 3u : 1u;
             }
         }
+        if (lane == 0) bulk_wait_all();
     }
 
     __syncwarp();
@@ -793,17 +1102,19 @@ EncodeTiledFn grouped_encode_fn()
     return fn;
 }
 
-// 16-bit map over [depth x rows x cols] with 128-byte swizzled boxes of 64 columns by box_rows rows.
+// Map over [depth x rows x cols] (depth 0: two dimensions) with boxes of 128 swizzled bytes by box_rows rows.
 bool encode(CUtensorMap *m, int type, const void *base, int cols, int64_t rows, int64_t ld, int depth, int64_t stride,
             int box_rows)
 {
     EncodeTiledFn fn = grouped_encode_fn();
     if (!fn) return false;
+    const int size = type == SF_TYPE_F32 ? 4 : 2;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)(rows > 0 ? rows : 1), (cuuint64_t)depth};
-    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {64u, (cuuint32_t)box_rows, 1u};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * size, (cuuint64_t)stride * size};
+    const cuuint32_t box[3] = {128u / size, (cuuint32_t)box_rows, 1u};
     const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(m, type == SF_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+    return fn(m, type == SF_TYPE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                 : type == SF_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
               depth > 0 ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
@@ -830,13 +1141,13 @@ int check_grouped(const sf_grouped *p, bool dw)
     if (p->ld_w > far || p->stride_w > far || p->ld_a > far || p->ld_y > far) return SF_ERR_UNSUPPORTED;
     const int64_t wide = (p->R > p->C ? p->R : p->C) / 128 + 1;
     const int64_t tall = (int64_t)p->T / 16 + p->E;
-    if (wide * tall > (1 << 30) || (int64_t)p->E * ((p->R + PM - 1) / PM) * ((p->C + PN - 1) / PN) > (1 << 30))
+    if (wide * tall > (1 << 30) || (int64_t)p->E * ((p->R + PM - 1) / PM) * ((p->C + 63) / 64) > (1 << 30))
         return SF_ERR_UNSUPPORTED;
     return SF_OK;
 }
 
-// CTA pairs that can be resident at once on the current device (the same for the three pair kernels: their
-// threads and shared memory agree).
+// CTA pairs that can be resident at once on the current device (the same for all pair kernels: a pair takes two
+// whole SMs).
 int pair_slots()
 {
     constexpr int kDevs = 64;
@@ -850,7 +1161,7 @@ int pair_slots()
     const int sms = sm_count();
     if (sms <= 0) return 0;
     if (cudaFuncSetAttribute(grouped_pair_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)P_SMEM_BYTES) != cudaSuccess)
+                             (int)T_SMEM_BYTES) != cudaSuccess)
         return 0;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -860,7 +1171,7 @@ int pair_slots()
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * sms);
     cfg.blockDim = dim3(P_THREADS);
-    cfg.dynamicSmemBytes = P_SMEM_BYTES;
+    cfg.dynamicSmemBytes = T_SMEM_BYTES;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
@@ -928,7 +1239,7 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
         if (slots <= 0) return SF_ERR_CUDA;
         const int64_t most = ((int64_t)p->T / 64 + p->E) * ((g.M + PM - 1) / PM);
         const int pairs = (int)(most < slots ? most : slots);
-        return launch(grouped_pair_kernel<TRANS>, 2 * pairs, 2, P_THREADS, P_SMEM_BYTES, g, status, stream);
+        return launch(grouped_pair_kernel<TRANS>, 2 * pairs, 2, P_THREADS, T_SMEM_BYTES, g, status, stream);
     }
     // a box of twice the average tokens holds nearly every expert in one tile
     const int avg = (p->T + p->E - 1) / p->E;
@@ -975,9 +1286,6 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
     GArgs g;
     memset(&g, 0, sizeof(g));
     g.offsets = p->offsets;
-    g.out = p->W;
-    g.ld_out = p->ld_w;
-    g.stride_out = p->E > 1 ? p->stride_w : 0;
     g.E = p->E;
     g.T = p->T;
     g.M = p->R;
@@ -988,11 +1296,13 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
     // without tokens nothing is loaded: any valid address makes the maps
     const void *a = p->T > 0 ? p->A : p->W, *y = p->T > 0 ? p->Y : p->W;
     const int64_t ld_a = p->T > 0 ? p->ld_a : p->C, ld_y = p->T > 0 ? p->ld_y : p->R;
-    if (!encode(&g.tm_w, p->type, a, p->C, p->T, ld_a, 0, 0, 64) || !encode(&g.tm_x, p->type, y, p->R, p->T, ld_y, 0, 0, 64))
+    const int64_t stride = p->E > 1 ? p->stride_w : (int64_t)p->R * p->ld_w;
+    if (!encode(&g.tm_w, p->type, a, p->C, p->T, ld_a, 0, 0, 64) || !encode(&g.tm_x, p->type, y, p->R, p->T, ld_y, 0, 0, 64) ||
+        !encode(&g.tm_out, p->w_type, p->W, p->C, p->R, p->ld_w, p->E, stride, 32))
         return SF_ERR_CUDA;
     const int slots = pair_slots();
     if (slots <= 0) return SF_ERR_CUDA;
-    const int64_t units = (int64_t)p->E * ((p->R + PM - 1) / PM) * ((p->C + PN - 1) / PN);
-    return launch(grouped_dw_kernel, 2 * (int)(units < slots ? units : slots), 2, P_THREADS, P_SMEM_BYTES, g, dev_status,
+    const int64_t units = (int64_t)p->E * ((p->R + PM - 1) / PM) * ((p->C + 31) / 32);      // at most
+    return launch(grouped_dw_kernel, 2 * (int)(units < slots ? units : slots), 2, W_THREADS, W_SMEM_BYTES, g, dev_status,
                   stream);
 }
