@@ -401,19 +401,6 @@ template <int N>
 SF_DEVICE void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
 SF_DEVICE void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// The address of the caller's shared-memory location in CTA `rank` of the cluster, and a store to one.
-SF_DEVICE uint32_t mapa_u32(uint32_t addr, uint32_t rank)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-
-SF_DEVICE void st_cluster_u32(uint32_t addr, uint32_t v)
-{
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
 // Every thread of every CTA of the cluster arrives, then waits for all of them.
 SF_DEVICE void cluster_sync()
 {
