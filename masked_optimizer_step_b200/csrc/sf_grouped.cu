@@ -42,7 +42,11 @@ constexpr int T_STAGE_BYTES = 3 * P_HALF_BYTES;
 constexpr int T_OUT_BYTES = 32 * 128 * 2;     // forward, dx: 32 tokens' rows of the CTA's 128 features, on their way out
 constexpr int W_OUT_BYTES = 32 * 128;         // weight gradient: 32 rows of 128 bytes of a warp's output
 constexpr size_t T_SMEM_BYTES = (size_t)T_STAGES * T_STAGE_BYTES + 2 * T_OUT_BYTES + 1024;
-constexpr size_t W_SMEM_BYTES = (size_t)T_STAGES * T_STAGE_BYTES + P_EPI_WARPS * W_OUT_BYTES + 1024;
+// weight gradient: 256 columns to a tile, two accumulators that the MMAs and the epilogue take in turn
+constexpr int W_STAGES_NEW = 6, W_STAGES_OLD = 3;
+constexpr int W_STAGE_BYTES = 2 * P_HALF_BYTES;
+constexpr size_t W_SMEM_BYTES = (size_t)W_STAGES_NEW * W_STAGE_BYTES + P_EPI_WARPS * W_OUT_BYTES + 1024;
+static_assert(W_SMEM_BYTES == (size_t)W_STAGES_OLD * W_STAGE_BYTES + P_EPI_WARPS * 4 * W_OUT_BYTES + 1024, "both divisions");
 constexpr int T_AHEAD = 3;                    // stages of a unit whose first halves run before any second half
 constexpr int T_BAND = 4;                     // token tiles that share a pass over an expert's weights
 
@@ -52,6 +56,9 @@ constexpr int S_EPI_WARPS = 4;
 constexpr int S_THREADS = 64 + 32 * S_EPI_WARPS;
 constexpr int S_W_BYTES = SM_ROWS * GK * 2;   // 16 KB
 constexpr int S_MAX_STAGES = 12;
+constexpr int D_THREADS = P_THREADS;          // weight gradient: TMA, MMA and eight epilogue warps
+constexpr int D_STAGE_BYTES = 3 * P_HALF_BYTES;
+constexpr int D_MAX_STAGES = 4;
 
 
 // Weight gradient, fp32: tokens that the tensor core sums before the sums are added in fp32, in stages. It adds with
@@ -68,8 +75,8 @@ struct GArgs {
     CUtensorMap tm_x;          // tokens: forward A, dx Y as {K, T}; dw: Y as {R, T}
     CUtensorMap tm_out;        // dw: W as {C, R, E}, boxes of 128 bytes x 32 rows
     const int32_t *offsets;
-    void *out;                 // forward, dx
-    int64_t ld_out;
+    void *out;
+    int64_t ld_out, stride_out;
     int32_t E, T, M, K, type;  // M: accumulator rows in all (forward R, dx C, dw R); K: forward C, dx R, dw C (its N)
     int32_t nb, stages;              // single CTAs: token box, stages
     int32_t out_f32, accumulate;     // dw
@@ -315,7 +322,6 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         prefetch_tmap(&g.tm_w);
         prefetch_tmap(&g.tm_x);
     }
-    griddep_wait();                               // what the launches before this one wrote is there from here on
     if (!load_offsets(pl, g.offsets, g.E, g.T)) {     // both CTAs of every pair see the same offsets
         if (blockIdx.x == 0 && tid == 0) set_status(status, SF_STATUS_BAD_OFFSET);
         return;
@@ -328,7 +334,6 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    griddep_launch_dependents();                // after the allocation, as in the small kernel
     const uint32_t tmem_base = tmem_base_s;
     const int total_units = pl.pre[g.E];
     const int nk = (g.K + GK - 1) / GK;
@@ -732,7 +737,6 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 
 struct WUnit {
     int e, r0, c0, t0, cnt;    // expert, first row, first column, first token, tokens
-    int n0, n1;                // columns of the two halves (steps of 32; n1 may be 0)
     int nk, chunks, per;       // stages of 64 tokens, accumulation chunks, stages to a chunk
 };
 
@@ -743,32 +747,36 @@ struct WPlan {
 
 __device__ __forceinline__ WUnit dw_unit(const WPlan &pl, const GArgs &g, int u)
 {
-    const int tile = tile_tokens(g.K, T_TOKENS, 64), n_tiles = quot_up(g.K, tile);
-    const int m_tiles = (g.M + PM - 1) / PM, per = m_tiles * n_tiles;
+    const int n_tiles = (g.K + PN - 1) / PN, per = (g.M + PM - 1) / PM * n_tiles;
     WUnit x;
     const int place = quot(u, per), local = u - place * per, mt = quot(local, n_tiles);
     x.e = g.E <= kSortE ? pl.order[place] : place;
     x.r0 = mt * PM;
-    x.c0 = (local - mt * n_tiles) * tile;
-    const int n = (min(tile, g.K - x.c0) + 31) & ~31;
-    x.n0 = min(n, PN);
-    x.n1 = n - x.n0;
+    x.c0 = (local - mt * n_tiles) * PN;
     x.t0 = __ldg(g.offsets + x.e);
     x.cnt = __ldg(g.offsets + x.e + 1) - x.t0;
     x.nk = (x.cnt + GK - 1) / GK;
-    x.chunks = g.out_f32 ? quot_up(x.nk, W_CHUNK_STAGES) : min(x.nk, 1);
+    x.chunks = quot_up(x.nk, W_CHUNK_STAGES);
     x.per = x.chunks ? quot_up(x.nk, x.chunks) : 0;
     return x;
 }
 
 __device__ __forceinline__ bool has_tail(const WUnit &x) { return (x.cnt & (G_UMMA_K - 1)) != 0; }
 
+// OLD: for gradients that are added to, over few tokens. What W holds comes into the output boxes by TMA while the MMAs
+// run, is added there and goes out by TMA: the time is that of reading and writing W once, with fewer stages for the
+// tokens and a place for all of a warp's boxes. Otherwise the addition is TMA's, at 2.4 TB/s of results: 321 us against
+// 392 .. (see the launch) where the tokens take longer than W.
+template <bool OLD>
 __global__ void __launch_bounds__(W_THREADS, 1)
 grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 {
+    constexpr int W_STAGES = OLD ? W_STAGES_OLD : W_STAGES_NEW;
+    constexpr int BOXES = OLD ? 4 : 1;          // output boxes of a warp in shared memory
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full_bar[T_STAGES], empty_bar[T_STAGES], tfull_bar[2], tempty_bar[2], drain_bar;
-    __shared__ uint64_t tail_bar[T_STAGES], clear_bar[T_STAGES];   // for the last stage of an expert, where rows are cleared
+    __shared__ uint64_t full_bar[W_STAGES], empty_bar[W_STAGES], tfull_bar[2], tempty_bar[2], drain_bar;
+    __shared__ uint64_t tail_bar[W_STAGES], clear_bar[W_STAGES];   // for the last stage of an expert, where rows are cleared
+    __shared__ uint64_t old_bar[P_EPI_WARPS];   // OLD: what W holds has landed, by warp
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile int abort_flag;
     __shared__ WPlan pl;
@@ -782,7 +790,7 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 
     if (tid == 0) {
         abort_flag = 0;
-        for (int s = 0; s < T_STAGES; ++s) {
+        for (int s = 0; s < W_STAGES; ++s) {
             mbar_init(&full_bar[s], 1);
             mbar_init(&empty_bar[s], 1);
             mbar_init(&tail_bar[s], 1);           // this CTA's loads of the stage have landed
@@ -793,17 +801,17 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
             mbar_init(&tempty_bar[a], P_EPI_WARPS * 2);
         }
         mbar_init(&drain_bar, 1);
+        for (int w = 0; w < P_EPI_WARPS; ++w) mbar_init(&old_bar[w], 1);
         fence_mbarrier_init();
         prefetch_tmap(&g.tm_w);
         prefetch_tmap(&g.tm_x);
         prefetch_tmap(&g.tm_out);
     }
-    griddep_wait();
-    int busy;                                   // experts with tokens
+    int busy = 0;                               // experts with tokens
     {   // offsets: valid, and the experts' order
         int bad = 0, some = 0;
         int *keys = reinterpret_cast<int *>(smem);                  // before the stages are used
-        for (int e = tid; e < g.E; e += blockDim.x) {
+        for (int e = tid; e < g.E; e += W_THREADS) {
             const int o0 = g.offsets[e], o1 = g.offsets[e + 1];
             if (o0 < 0 || o1 < o0 || o1 > g.T) bad = 1;
             some += o1 > o0;
@@ -815,10 +823,9 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
             if (blockIdx.x == 0 && tid == 0) set_status(status, SF_STATUS_BAD_OFFSET);
             return;
         }
-        busy = 0;
         for (int w = 0; w < W_THREADS / 32; ++w) busy += warp_busy[w];
         if (g.E <= kSortE)
-            for (int e = tid; e < g.E; e += blockDim.x) {
+            for (int e = tid; e < g.E; e += W_THREADS) {
                 const int mine = keys[e];
                 int rank = 0;
                 for (int k = 0; k < g.E; ++k) rank += keys[k] > mine || (keys[k] == mine && k < e);
@@ -832,61 +839,49 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    griddep_launch_dependents();                // after the allocation, as in the small kernel
     const uint32_t tmem_base = tmem_base_s;
-    const int tile_c = tile_tokens(g.K, T_TOKENS, 64);
     // experts without tokens are the last in the order; a gradient that is added to has nothing to do for them
     const int places = g.accumulate && g.E <= kSortE ? busy : g.E;
-    const int total_units = places * ((g.M + PM - 1) / PM) * quot_up(g.K, tile_c);
+    const int total_units = places * ((g.M + PM - 1) / PM) * ((g.K + PN - 1) / PN);
 
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            bool issued[T_STAGES] = {};
-            uint32_t issued_parity[T_STAGES] = {};
+            bool issued[W_STAGES] = {};
+            uint32_t issued_parity[W_STAGES] = {};
             uint32_t tails = 0, tail_parity = 0;  // by stage: whether it held a tail, and the parity of its last one
             bool ok = true;
             for (int i = 0; i * workers < total_units && ok; ++i) {
                 const int u = unit_of(i, worker, workers);
                 if (u >= total_units) break;
                 const WUnit x = dw_unit(pl, g, u);
-                const int r = x.r0 + (int)crank * 128;
-                const int ca = x.c0 + (int)crank * (x.n0 / 2), cb = x.c0 + x.n0 + (int)crank * (x.n1 / 2);
-                const uint32_t bytes = (uint32_t)P_HALF_BYTES * (x.n1 ? 3 : 2);
+                const int r = x.r0 + (int)crank * 128, c = x.c0 + (int)crank * 128;
                 for (int kb = 0; kb < x.nk; ++kb) {
                     if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag)) { ok = false; break; }
-                    uint8_t *sy = smem + stage * T_STAGE_BYTES, *sa = sy + P_HALF_BYTES, *sb = sa + P_HALF_BYTES;
+                    uint8_t *sy = smem + stage * W_STAGE_BYTES, *sa = sy + P_HALF_BYTES;
                     const int t = x.t0 + kb * GK;
                     if (kb == x.nk - 1 && has_tail(x)) {
                         // rows to clear: each CTA's loads complete on its own barrier, for the warp that clears them
                         if (leader) mbar_arrive(&full_bar[stage]);
-                        mbar_arrive_expect_tx(&tail_bar[stage], bytes);
+                        mbar_arrive_expect_tx(&tail_bar[stage], W_STAGE_BYTES);
                         tma_load_2d(sy, &g.tm_x, &tail_bar[stage], r, t);
                         tma_load_2d(sy + G_BOX_BYTES, &g.tm_x, &tail_bar[stage], r + 64, t);
-                        tma_load_2d(sa, &g.tm_w, &tail_bar[stage], ca, t);
-                        tma_load_2d(sa + G_BOX_BYTES, &g.tm_w, &tail_bar[stage], ca + 64, t);
-                        if (x.n1) {
-                            tma_load_2d(sb, &g.tm_w, &tail_bar[stage], cb, t);
-                            tma_load_2d(sb + G_BOX_BYTES, &g.tm_w, &tail_bar[stage], cb + 64, t);
-                        }
+                        tma_load_2d(sa, &g.tm_w, &tail_bar[stage], c, t);
+                        tma_load_2d(sa + G_BOX_BYTES, &g.tm_w, &tail_bar[stage], c + 64, t);
                         if (tails >> stage & 1u) tail_parity ^= 1u << stage;
                         tails |= 1u << stage;
                     } else {
-                        if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * bytes);
+                        if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * W_STAGE_BYTES);
                         tma_load_2d_pair(sy, &g.tm_x, &full_bar[stage], r, t);
                         tma_load_2d_pair(sy + G_BOX_BYTES, &g.tm_x, &full_bar[stage], r + 64, t);
-                        tma_load_2d_pair(sa, &g.tm_w, &full_bar[stage], ca, t);
-                        tma_load_2d_pair(sa + G_BOX_BYTES, &g.tm_w, &full_bar[stage], ca + 64, t);
-                        if (x.n1) {
-                            tma_load_2d_pair(sb, &g.tm_w, &full_bar[stage], cb, t);
-                            tma_load_2d_pair(sb + G_BOX_BYTES, &g.tm_w, &full_bar[stage], cb + 64, t);
-                        }
+                        tma_load_2d_pair(sa, &g.tm_w, &full_bar[stage], c, t);
+                        tma_load_2d_pair(sa + G_BOX_BYTES, &g.tm_w, &full_bar[stage], c + 64, t);
                     }
                     issued[stage] = true;
                     issued_parity[stage] = phase;
-                    if (++stage == T_STAGES) { stage = 0; phase ^= 1u; }
+                    if (++stage == W_STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
             {
@@ -895,13 +890,13 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
             }
             if (!ok || abort_flag) {
                 if (leader) {
-                    for (int s = 0; s < T_STAGES; ++s) {
+                    for (int s = 0; s < W_STAGES; ++s) {
                         if (!issued[s]) continue;
                         const uint64_t t0 = globaltimer_ns();
                         while (!mbar_try_wait(&full_bar[s], issued_parity[s]) && globaltimer_ns() - t0 < kWaitLimitNs) {}
                     }
                 }
-                for (int s = 0; s < T_STAGES; ++s) {
+                for (int s = 0; s < W_STAGES; ++s) {
                     if (!(tails >> s & 1u)) continue;
                     const uint64_t t0 = globaltimer_ns();
                     while (!mbar_try_wait(&tail_bar[s], tail_parity >> s & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {}
@@ -911,74 +906,48 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
         if (leader) {
-            int stage = 0;
-            uint32_t phase = 0, half_phase = 0, clear_phase = 0;   // a bit a half; a bit a stage
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, buf_phase = 0, clear_phase = 0;    // clear_phase: a bit a stage
             bool ok = true;
             const uint32_t s0 = smem_u32(smem);
             const uint64_t y0 = mnmajor(s0), a0 = mnmajor(s0 + P_HALF_BYTES);
-            auto half_stage = [&](int h, int st, uint32_t id, int steps, bool first, bool last, bool release) {
-                const uint64_t dy = y0 + (uint64_t)(st * (T_STAGE_BYTES >> 4));
-                const uint64_t da = a0 + (uint64_t)(st * (T_STAGE_BYTES >> 4) + h * (P_HALF_BYTES >> 4));
-                if (elect_one()) {
-                    if (steps == GK / G_UMMA_K) {
-#pragma unroll
-                        for (int k = 0; k < GK / G_UMMA_K; ++k)
-                            mma_bf16_pair(tmem_base + h * PN, dy + k * 128, da + k * 128, id, !first || k != 0);
-                    } else {
-                        for (int k = 0; k < steps; ++k)
-                            mma_bf16_pair(tmem_base + h * PN, dy + k * 128, da + k * 128, id, !first || k != 0);
-                    }
-                    if (last) mma_commit_pair(&tfull_bar[h], 3);
-                    if (release) mma_commit_pair(&empty_bar[st], 3);
-                }
-                __syncwarp();
-            };
+            const uint32_t id = idesc(g.type, true, true, PN, PM);
             for (int i = 0; i * workers < total_units && ok; ++i) {
                 const int u = unit_of(i, worker, workers);
                 if (u >= total_units) break;
                 const WUnit x = dw_unit(pl, g, u);
-                const uint32_t id0 = idesc(g.type, true, true, x.n0, PM), id1 = idesc(g.type, true, true, x.n1, PM);
-                const int rest = x.cnt - (x.nk - 1) * GK;               // tokens of the last stage
-                auto steps_of = [&](int kb) { return kb == x.nk - 1 ? (rest + G_UMMA_K - 1) / G_UMMA_K : GK / G_UMMA_K; };
-                // Waits for stage kb in slot st; the last one also for the cleared rows.
-                auto arrived = [&](int kb, int st, uint32_t ph) {
-                    bool there = mbar_wait(&full_bar[st], ph, &abort_flag);
-                    if (there && kb == x.nk - 1 && has_tail(x)) {
-                        there = mbar_wait_cluster(&clear_bar[st], clear_phase >> st & 1u, &abort_flag);
-                        clear_phase ^= 1u << st;
-                    }
-                    return __all_sync(0xffffffffu, there) != 0;
-                };
-                for (int ch = 0; ch < x.chunks && ok; ++ch) {
-                    const int begin = ch * x.per, end = min(x.nk, begin + x.per);
-                    ok = __all_sync(0xffffffffu, mbar_wait(&tempty_bar[0], (half_phase & 1u) ^ 1u, &abort_flag));
+                for (int ch = 0, kb = 0; ch < x.chunks && ok; ++ch) {
+                    const int end = min(x.nk, kb + x.per);
+                    const uint32_t d_tmem = tmem_base + (uint32_t)(buf * PN);
+                    ok = __all_sync(0xffffffffu, mbar_wait(&tempty_bar[buf], buf_phase ^ 1u, &abort_flag));
                     if (!ok) break;
-                    // as in the forward kernel: first halves of the first stages, then their second halves
-                    const int ahead = x.n1 ? begin + min(T_AHEAD, end - begin) : begin;
-                    int kb = begin;
-                    for (; kb < ahead && ok; ++kb) {
-                        const int at = stage + kb - begin, st = at < T_STAGES ? at : at - T_STAGES;
-                        ok = arrived(kb, st, at < T_STAGES ? phase : phase ^ 1u);
+                    for (bool first = true; kb < end; ++kb, first = false) {
+                        const bool tail = kb == x.nk - 1 && has_tail(x);
+                        bool there = mbar_wait(&full_bar[stage], phase, &abort_flag);
+                        if (there && tail) there = mbar_wait_cluster(&clear_bar[stage], clear_phase >> stage & 1u, &abort_flag);
+                        ok = __all_sync(0xffffffffu, there);
                         if (!ok) break;
+                        if (tail) clear_phase ^= 1u << stage;
                         tc_fence_after();
-                        half_stage(0, st, id0, steps_of(kb), kb == begin, kb == end - 1, false);
+                        const uint64_t dy = y0 + (uint64_t)(stage * (W_STAGE_BYTES >> 4));
+                        const uint64_t da = a0 + (uint64_t)(stage * (W_STAGE_BYTES >> 4));
+                        const int rest = x.cnt - kb * GK;
+                        if (elect_one()) {
+                            if (rest >= GK) {
+#pragma unroll
+                                for (int k = 0; k < GK / G_UMMA_K; ++k)
+                                    mma_bf16_pair(d_tmem, dy + k * 128, da + k * 128, id, !first || k != 0);
+                            } else {
+                                for (int k = 0; k * G_UMMA_K < rest; ++k)
+                                    mma_bf16_pair(d_tmem, dy + k * 128, da + k * 128, id, !first || k != 0);
+                            }
+                            mma_commit_pair(&empty_bar[stage], 3);
+                            if (kb == end - 1) mma_commit_pair(&tfull_bar[buf], 3);
+                        }
+                        __syncwarp();
+                        if (++stage == W_STAGES) { stage = 0; phase ^= 1u; }
                     }
-                    if (ok && x.n1) ok = __all_sync(0xffffffffu, mbar_wait(&tempty_bar[1], (half_phase >> 1) ^ 1u, &abort_flag));
-                    if (!ok) break;
-                    tc_fence_after();
-                    for (kb = begin; kb < ahead; ++kb) {
-                        half_stage(1, stage, id1, steps_of(kb), kb == begin, kb == end - 1, true);
-                        if (++stage == T_STAGES) { stage = 0; phase ^= 1u; }
-                    }
-                    for (; kb < end; ++kb) {
-                        ok = arrived(kb, stage, phase);
-                        if (!ok) break;
-                        tc_fence_after();
-                        half_stage(0, stage, id0, steps_of(kb), kb == begin, kb == end - 1, x.n1 == 0);
-                        if (x.n1) half_stage(1, stage, id1, steps_of(kb), false, kb == end - 1, true);
-                        if (++stage == T_STAGES) { stage = 0; phase ^= 1u; }
-                    }
-                    half_phase ^= x.n1 ? 3u : 1u;
+                    if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
                 }
             }
             if (elect_one()) mma_commit_pair(&drain_bar, 3);
@@ -995,15 +964,15 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
             if (u >= total_units) break;
             const WUnit x = dw_unit(pl, g, u);
             if (has_tail(x)) {
-                const int st = (stage + x.nk - 1) % T_STAGES;
+                const int st = (stage + x.nk - 1) % W_STAGES;
                 if (!__all_sync(0xffffffffu, mbar_wait(&tail_bar[st], tail_phase >> st & 1u, &abort_flag))) break;
                 tail_phase ^= 1u << st;
                 const int from = x.cnt - (x.nk - 1) * GK, upto = (from + G_UMMA_K - 1) & ~(G_UMMA_K - 1);
-                uint8_t *sy = smem + st * T_STAGE_BYTES;
+                uint8_t *sy = smem + st * W_STAGE_BYTES;
                 // a token is one 128-byte row of each of the stage's boxes
                 for (int j = lane; j < (upto - from) * 8; j += 32)
 #pragma unroll
-                    for (int q = 0; q < T_STAGE_BYTES / G_BOX_BYTES; ++q)
+                    for (int q = 0; q < W_STAGE_BYTES / G_BOX_BYTES; ++q)
                         *reinterpret_cast<uint4 *>(sy + q * G_BOX_BYTES + (from + (j >> 3)) * 128 + (j & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
@@ -1013,105 +982,111 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                     else mbar_arrive_remote(&clear_bar[st], 0);
                 }
             }
-            stage = (stage + x.nk) % T_STAGES;
+            stage = (stage + x.nk) % W_STAGES;
         }
     } else {
         // --------------------------- epilogue (warps 2..9) ---------------------------
         const int quad = warp & 3;              // accumulator rows 32*quad .. 32*quad+31 of the CTA
-        const int part = (warp - 2) >> 2;       // 128 of a half's columns
-        uint8_t *s_out = smem + T_STAGES * T_STAGE_BYTES + (warp - 2) * W_OUT_BYTES;
-        uint4 *slot = reinterpret_cast<uint4 *>(s_out) + lane * 8;
-        uint32_t half_phase = 0;
-        bool ready = true;
-        for (int i = 0; i * workers < total_units && ready; ++i) {
+        const int part = (warp - 2) >> 2;       // columns part*128 .. +127
+        uint8_t *s_warp = smem + W_STAGES * W_STAGE_BYTES + (warp - 2) * BOXES * W_OUT_BYTES;
+        int buf = 0;
+        uint32_t buf_phase = 0, old_phase = 0;
+        for (int i = 0; i * workers < total_units; ++i) {
             const int u = unit_of(i, worker, workers);
             if (u >= total_units) break;
             const WUnit x = dw_unit(pl, g, u);
-            const int row0 = x.r0 + (int)crank * 128 + quad * 32;
-            if (x.chunks == 0) {                // an expert without tokens
-                if (g.accumulate || row0 >= g.M) continue;
-                if (lane == 0) bulk_wait_read<0>();
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 8; ++j) slot[j] = make_uint4(0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-                const int box = g.out_f32 ? 32 : 64;
-                if (lane == 0) {
-                    for (int c = x.c0 + part * 128; c < min(x.c0 + x.n0 + x.n1, g.K); c += box) {
-                        if (((c - x.c0) & 128) != part * 128) continue;
-                        tma_store_3d(&g.tm_out, s_out, c, row0, x.e);
-                    }
-                    bulk_commit();
-                }
-                continue;
+            if (x.nk == 0 && g.accumulate) continue;
+            const int row0 = x.r0 + (int)crank * 128 + quad * 32, c0 = x.c0 + part * 128;
+            const int boxes = row0 < g.M ? min(4, (g.K - c0 + 31) / 32) : 0;     // of 32 x 32 that W has here
+            if (OLD && boxes > 0 && lane == 0) {
+                bulk_wait_read<0>();
+                mbar_arrive_expect_tx(&old_bar[warp - 2], boxes * W_OUT_BYTES);
+                for (int q = 0; q < boxes; ++q)
+                    tma_load_3d(s_warp + q * W_OUT_BYTES, &g.tm_out, &old_bar[warp - 2], c0 + q * 32, row0, x.e);
             }
-            for (int ch = 0; ch < x.chunks && ready; ++ch) {
-                const bool add = g.accumulate || ch > 0;
-                for (int h = 0; h < (x.n1 ? 2 : 1); ++h) {
-                    ready = __all_sync(0xffffffffu, mbar_wait(&tfull_bar[h], half_phase >> h & 1u, &abort_flag));
-                    if (!ready) break;
-                    tc_fence_after();
-                    // all of this warp's columns into registers, so that the MMAs get the accumulator back at once
-                    // (columns behind the half's last hold what an earlier tile left, and are not stored)
-                    const uint32_t t_row = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(h * PN + part * 128);
-                    uint32_t v[4][32];
+            float acc[128];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(t_row + q * 32, v[q]);
+            for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+            bool ready = true;
+            for (int ch = 0; ch < x.chunks; ++ch) {
+                ready = __all_sync(0xffffffffu, mbar_wait(&tfull_bar[buf], buf_phase, &abort_flag));
+                if (!ready) break;
+                tc_fence_after();
+                const uint32_t t_row = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * PN + part * 128);
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(t_row + cc * 32, v);
                     tmem_ld_wait();
-                    tc_fence_before();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[cc * 32 + j] = __fadd_rn(acc[cc * 32 + j], __uint_as_float(v[j]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader) mbar_arrive(&tempty_bar[buf]);
+                    else mbar_arrive_remote(&tempty_bar[buf], 0);
+                }
+                if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+            }
+            if (OLD && boxes > 0) {             // also where the MMAs gave up: these loads end in this shared memory
+                ready = __all_sync(0xffffffffu, mbar_wait(&old_bar[warp - 2], old_phase, &abort_flag)) && ready;
+                old_phase ^= 1u;
+            }
+            if (!ready) break;
+            if (boxes <= 0) continue;
+            // Out through shared memory, a box of 32 rows x 128 bytes at a time (16-byte units swizzled by row, as
+            // the tensor map has it): what lies outside W the store leaves out.
+            if (g.out_f32) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (q >= boxes) break;
+                    uint8_t *s_out = s_warp + (OLD ? q * W_OUT_BYTES : 0);
+                    float4 *slot = reinterpret_cast<float4 *>(s_out) + lane * 8;
+                    if (!OLD) {
+                        if (lane == 0) bulk_wait_read<0>();
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float4 v = make_float4(acc[q * 32 + 4 * j], acc[q * 32 + 4 * j + 1], acc[q * 32 + 4 * j + 2], acc[q * 32 + 4 * j + 3]);
+                        if (OLD) {
+                            const float4 o = slot[j ^ (lane & 7)];
+                            v = make_float4(__fadd_rn(o.x, v.x), __fadd_rn(o.y, v.y), __fadd_rn(o.z, v.z), __fadd_rn(o.w, v.w));
+                        }
+                        slot[j ^ (lane & 7)] = v;
+                    }
+                    fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        if (leader) mbar_arrive(&tempty_bar[h]);
-                        else mbar_arrive_remote(&tempty_bar[h], 0);
-                    }
-                    const int c0 = x.c0 + h * PN + part * 128;
-                    const int cols = row0 < g.M ? min((h ? x.n1 : x.n0) - part * 128, g.K - c0) : 0;
-                    // A later chunk is added to what the chunk before left: that has to be there.
-                    if (ch > 0 && h == 0 && lane == 0) bulk_wait_all();
-                    // Out through shared memory, a box of 32 rows x 128 bytes at a time (16-byte units swizzled by
-                    // row, as the tensor map has it): what lies outside W the store leaves out.
-                    if (g.out_f32) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (q * 32 >= cols) break;
-                            if (lane == 0) bulk_wait_read<0>();
-                            __syncwarp();
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                slot[j ^ (lane & 7)] = make_uint4(v[q][4 * j], v[q][4 * j + 1], v[q][4 * j + 2], v[q][4 * j + 3]);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) {
-                                if (add) tma_add_3d(&g.tm_out, s_out, c0 + q * 32, row0, x.e);
-                                else tma_store_3d(&g.tm_out, s_out, c0 + q * 32, row0, x.e);
-                                bulk_commit();
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            if (q * 64 >= cols) break;
-                            if (lane == 0) bulk_wait_read<0>();
-                            __syncwarp();
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    w[k] = pack2(v[2 * q + j / 4][8 * (j & 3) + 2 * k], v[2 * q + j / 4][8 * (j & 3) + 2 * k + 1], g.type);
-                                slot[j ^ (lane & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) {
-                                tma_store_3d(&g.tm_out, s_out, c0 + q * 64, row0, x.e);
-                                bulk_commit();
-                            }
-                        }
+                        if (!OLD && g.accumulate) tma_add_3d(&g.tm_out, s_out, c0 + q * 32, row0, x.e);
+                        else tma_store_3d(&g.tm_out, s_out, c0 + q * 32, row0, x.e);
+                        bulk_commit();
                     }
                 }
-                half_phase ^= x.n1 ? 3u : 1u;
+            } else if (!OLD) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (2 * q >= boxes) break;
+                    uint8_t *s_out = s_warp;
+                    uint4 *slot = reinterpret_cast<uint4 *>(s_out) + lane * 8;
+                    if (lane == 0) bulk_wait_read<0>();
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = pack2(__float_as_uint(acc[q * 64 + 8 * j + 2 * k]), __float_as_uint(acc[q * 64 + 8 * j + 2 * k + 1]), g.type);
+                        slot[j ^ (lane & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d(&g.tm_out, s_out, c0 + q * 64, row0, x.e);
+                        bulk_commit();
+                    }
+                }
             }
         }
         if (lane == 0) bulk_wait_all();
@@ -1125,6 +1100,294 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, P_TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// weight gradient, few tokens to an expert or few tiles: a unit to a CTA, two CTAs to an SM
+// ------------------------------------------------------------------------------------------------
+
+// Adds a box of 32 rows x 128 bytes, laid down by its warp (lane = row, 16-byte units swizzled by row), to what W holds,
+// four rows of 128 bytes at a time, so that each access is whole lines. (TMA's addition moves 2.4 TB/s of results where
+// this moves 3.4: both read and write W.)
+__device__ __forceinline__ void add_box(const uint4 *box, float *dst, int64_t ld, int rows, int cols, int lane)
+{
+    float4 old[8];
+    const int col = (lane & 7) * 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = i * 4 + (lane >> 3);
+        old[i] = row < rows && col < cols ? *reinterpret_cast<const float4 *>(dst + row * ld + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = i * 4 + (lane >> 3);
+        const uint4 v = box[row * 8 + ((lane & 7) ^ (row & 7))];
+        if (row < rows && col < cols)
+            *reinterpret_cast<float4 *>(dst + row * ld + col) =
+                make_float4(__fadd_rn(old[i].x, __uint_as_float(v.x)), __fadd_rn(old[i].y, __uint_as_float(v.y)),
+                            __fadd_rn(old[i].z, __uint_as_float(v.z)), __fadd_rn(old[i].w, __uint_as_float(v.w)));
+    }
+}
+
+// A unit is 128 / S rows x 256 / S columns of one expert's W and all its tokens, in S slices of tokens as in the small
+// forward kernel: slice j in rows j * 128 / S .. of the M operand and columns j * 256 / S .. of the N operand, of whose
+// products the S blocks on the diagonal are wanted. While one CTA of an SM waits for its tokens the other writes.
+template <int S>
+__global__ void __launch_bounds__(D_THREADS, 2)
+grouped_dw_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full_bar[D_MAX_STAGES], empty_bar[D_MAX_STAGES], done_bar;
+    __shared__ uint32_t tmem_base_s;
+    __shared__ volatile int abort_flag;
+
+    constexpr int ROWS = SM_ROWS / S, COLS = PN / S;
+    constexpr int PITCH = COLS + 4;             // of the partial sums, in floats: rows start 4 banks apart
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int stages = g.stages;
+
+    if (tid == 0) {
+        prefetch_tmap(&g.tm_w);
+        prefetch_tmap(&g.tm_x);
+        abort_flag = 0;
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&full_bar[s], 1);
+            mbar_init(&empty_bar[s], 1);
+        }
+        mbar_init(&done_bar, 1);
+        fence_mbarrier_init();
+    }
+    if (warp == 1) tmem_alloc(&tmem_base_s, PN);
+    griddep_wait();                             // as in the small forward kernel
+    int bad = 0;
+    for (int e = tid; e < g.E; e += D_THREADS) {
+        const int o0 = g.offsets[e], o1 = g.offsets[e + 1];
+        if (o0 < 0 || o1 < o0 || o1 > g.T) bad = 1;
+    }
+    tc_fence_before();
+    bad = __syncthreads_or(bad);
+    tc_fence_after();
+    griddep_launch_dependents();
+    const uint32_t tmem_base = tmem_base_s;
+
+    const int n_tiles = (g.K + COLS - 1) / COLS, per = (g.M + ROWS - 1) / ROWS * n_tiles;
+    const int e = quot(blockIdx.x, per), local = blockIdx.x - e * per, mt = quot(local, n_tiles);
+    const int r0 = mt * ROWS, c0 = (local - mt * n_tiles) * COLS;
+    const int t0 = bad ? 0 : __ldg(g.offsets + e), cnt = bad ? 0 : __ldg(g.offsets + e + 1) - t0;
+    const int rows = min(ROWS, g.M - r0), cols = min(COLS, g.K - c0);
+    const int64_t at = (int64_t)e * g.stride_out + (int64_t)r0 * g.ld_out + c0;
+    float *w32 = static_cast<float *>(g.out) + at;
+    uint16_t *w16 = static_cast<uint16_t *>(g.out) + at;
+    if (bad || cnt == 0) {
+        if (bad) {
+            if (blockIdx.x == 0 && tid == 0) set_status(status, SF_STATUS_BAD_OFFSET);
+        } else if (!g.accumulate) {             // an expert without tokens: zeros, 16 bytes to a thread
+            const int unit = g.out_f32 ? 4 : 8, line = cols / unit;
+            for (int i = tid; i < rows * line; i += D_THREADS) {
+                const int r = quot(i, line), c = (i - r * line) * unit;
+                if (g.out_f32) *reinterpret_cast<uint4 *>(w32 + r * g.ld_out + c) = make_uint4(0u, 0u, 0u, 0u);
+                else *reinterpret_cast<uint4 *>(w16 + r * g.ld_out + c) = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+        __syncwarp();
+        if (warp == 1) tmem_dealloc(tmem_base, PN);
+        return;
+    }
+    if (g.accumulate)                           // what W holds, on its way while the MMAs run
+        for (int i = tid; i < rows * (COLS / 32); i += D_THREADS) {
+            const int r = i / (COLS / 32), c = (i - r * (COLS / 32)) * 32;
+            if (c < cols) prefetch_l2(w32 + r * g.ld_out + c);
+        }
+    const int nk = ((cnt + GK - 1) / GK + S - 1) / S;          // steps of each slice
+    const int chunks = g.out_f32 ? quot_up(nk, W_CHUNK_STAGES) : 1, chunk = quot_up(nk, chunks);
+    // slice j's tokens in its step i, those of the slice's end and of the expert's end left out
+    auto tokens_of = [&](int j, int i) { return min(GK, cnt - (j * nk + i) * GK); };
+    int stage = 0, sent = 0;
+    uint32_t phase = 0;
+    for (int ch = 0; ch < chunks; ++ch) {
+        const int begin = ch * chunk, end = min(nk, begin + chunk);
+        if (warp == 0) {
+            if (lane == 0) {
+                for (int i = begin; i < end; ++i) {
+                    if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag)) break;
+                    uint8_t *sy = smem + stage * D_STAGE_BYTES, *sa = sy + P_HALF_BYTES;
+                    mbar_arrive_expect_tx(&full_bar[stage], D_STAGE_BYTES);
+#pragma unroll
+                    for (int j = 0; j < S; ++j) {
+                        // a step behind the end reads behind the last row: zeros
+                        const int t = tokens_of(j, i) > 0 ? t0 + (j * nk + i) * GK : g.T;
+                        tma_load_2d(sy + j * (P_HALF_BYTES / S), &g.tm_x, &full_bar[stage], r0, t);
+                        if (S == 1) tma_load_2d(sy + G_BOX_BYTES, &g.tm_x, &full_bar[stage], r0 + 64, t);
+#pragma unroll
+                        for (int b = 0; b < COLS / 64; ++b)
+                            tma_load_2d(sa + (j * (COLS / 64) + b) * G_BOX_BYTES, &g.tm_w, &full_bar[stage], c0 + 64 * b, t);
+                    }
+                    ++sent;
+                    if (++stage == stages) { stage = 0; phase ^= 1u; }
+                }
+                const uint64_t from = globaltimer_ns();
+                while (!mbar_try_wait(&done_bar, (uint32_t)(ch & 1)) && globaltimer_ns() - from < kWaitLimitNs) {}
+            }
+        } else if (warp == 1) {
+            const uint32_t s0 = smem_u32(smem);
+            const uint64_t y0 = S == 4 ? mnmajor64(s0) : mnmajor(s0), a0 = mnmajor(s0 + P_HALF_BYTES);
+            const uint32_t id = idesc(g.type, true, true, S == 1 ? (cols + 15) & ~15 : PN, SM_ROWS);
+            int i = begin;
+            for (; i < end; ++i) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, &abort_flag))) break;
+                uint8_t *sy = smem + stage * D_STAGE_BYTES, *sa = sy + P_HALF_BYTES;
+#pragma unroll
+                for (int j = 0; j < S; ++j) {   // rows of the next expert, in the box that holds the end: cleared
+                    const int n = tokens_of(j, i);
+                    if (n <= 0 || n >= GK) continue;
+                    constexpr int ROW = S == 4 ? 64 : 128;            // bytes of a token in a box of the M operand
+                    for (int k = lane; k < (GK - n) * 8; k += 32) {
+                        const int row = n + (k >> 3);
+                        if ((k & 7) * 16 < ROW) {
+                            *reinterpret_cast<uint4 *>(sy + j * (P_HALF_BYTES / S) + row * ROW + (k & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            if (S == 1)
+                                *reinterpret_cast<uint4 *>(sy + G_BOX_BYTES + row * ROW + (k & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+#pragma unroll
+                        for (int b = 0; b < COLS / 64; ++b)
+                            *reinterpret_cast<uint4 *>(sa + (j * (COLS / 64) + b) * G_BOX_BYTES + row * 128 + (k & 7) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                tc_fence_after();
+                const uint64_t dy = y0 + (uint64_t)(stage * (D_STAGE_BYTES >> 4));
+                const uint64_t da = a0 + (uint64_t)(stage * (D_STAGE_BYTES >> 4));
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < GK / G_UMMA_K; ++k)
+                        mma_bf16(tmem_base, dy + k * (S == 4 ? 64 : 128), da + k * 128, id, i != begin || k != 0);
+                    mma_commit(&empty_bar[stage]);
+                    if (i == end - 1) mma_commit(&done_bar);
+                }
+                __syncwarp();
+                if (++stage == stages) { stage = 0; phase ^= 1u; }
+            }
+            if (i < end && elect_one()) mma_commit(&done_bar);    // gave up
+        }
+        __syncwarp();
+        if (!mbar_wait(&done_bar, (uint32_t)(ch & 1), &abort_flag)) abort_flag = 1;
+        __syncthreads();
+        if (abort_flag) break;
+        tc_fence_after();
+        const bool add = g.accumulate || ch > 0;
+        if (warp >= 2) {
+            const int quad = warp & 3, part = (warp - 2) >> 2;
+            const int slice = quad * S / 4;
+            // this warp's 32 accumulator rows and its half of the slice's columns
+            const uint32_t t_row = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(slice * COLS + part * (COLS / 2));
+            if (S == 1) {
+                // out through shared memory (the stages are free), a box of 32 rows x 128 bytes at a time
+                uint8_t *s_out = smem + (warp - 2) * W_OUT_BYTES;
+                uint4 *slot = reinterpret_cast<uint4 *>(s_out) + lane * 8;
+                const int wrows = rows - quad * 32, wcols = cols - part * (COLS / 2);
+                float *d32 = w32 + quad * 32 * g.ld_out + part * (COLS / 2);
+                uint16_t *d16 = w16 + quad * 32 * g.ld_out + part * (COLS / 2);
+                const int box = g.out_f32 ? 32 : 64;
+                for (int c = 0; c < min(COLS / 2, wcols) && wrows > 0; c += box) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(t_row + c, v);
+                    tmem_ld_wait();
+                    if (g.out_f32) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) slot[j ^ (lane & 7)] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (h == 1) {
+                                tmem_ld_32x32b_x32(t_row + c + 32, v);
+                                tmem_ld_wait();
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                slot[(4 * h + j) ^ (lane & 7)] =
+                                    make_uint4(pack2(v[8 * j], v[8 * j + 1], g.type), pack2(v[8 * j + 2], v[8 * j + 3], g.type),
+                                               pack2(v[8 * j + 4], v[8 * j + 5], g.type), pack2(v[8 * j + 6], v[8 * j + 7], g.type));
+                        }
+                    }
+                    __syncwarp();
+                    const uint4 *lines = reinterpret_cast<const uint4 *>(s_out);
+                    if (add) {
+                        add_box(lines, d32 + c, g.ld_out, wrows, wcols - c, lane);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int row = i * 4 + (lane >> 3), unit = lane & 7;
+                            const uint4 w = lines[row * 8 + (unit ^ (row & 7))];
+                            if (row >= wrows) continue;
+                            if (g.out_f32) {
+                                if (c + unit * 4 < wcols) *reinterpret_cast<uint4 *>(d32 + row * g.ld_out + c + unit * 4) = w;
+                            } else if (c + unit * 8 < wcols) {
+                                *reinterpret_cast<uint4 *>(d16 + row * g.ld_out + c + unit * 8) = w;
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+            } else {
+                // partial sums of the slices, [slice][row][column], then their sum in the slices' order
+                float *part_sums = reinterpret_cast<float *>(smem);
+                float *mine = part_sums + (quad * 32 + lane) * PITCH + part * (COLS / 2);
+#pragma unroll
+                for (int c = 0; c < COLS / 2; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(t_row + c, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint4 *>(mine + c + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                }
+                asm volatile("bar.sync 1, %0;" ::"r"(32 * P_EPI_WARPS) : "memory");
+                for (int i = tid - 64; i < ROWS * (COLS / 4); i += 32 * P_EPI_WARPS) {
+                    const int r = i / (COLS / 4), c = (i - r * (COLS / 4)) * 4;
+                    if (r >= rows || c >= cols) continue;
+                    float4 s = *reinterpret_cast<const float4 *>(part_sums + r * PITCH + c);
+#pragma unroll
+                    for (int j = 1; j < S; ++j) {
+                        const float4 a = *reinterpret_cast<const float4 *>(part_sums + (j * ROWS + r) * PITCH + c);
+                        s = make_float4(__fadd_rn(s.x, a.x), __fadd_rn(s.y, a.y), __fadd_rn(s.z, a.z), __fadd_rn(s.w, a.w));
+                    }
+                    if (g.out_f32) {
+                        float4 *dst = reinterpret_cast<float4 *>(w32 + r * g.ld_out + c);
+                        if (add) {
+                            const float4 o = *dst;
+                            s = make_float4(__fadd_rn(o.x, s.x), __fadd_rn(o.y, s.y), __fadd_rn(o.z, s.z), __fadd_rn(o.w, s.w));
+                        }
+                        *dst = s;
+                    } else {
+                        *reinterpret_cast<uint2 *>(w16 + r * g.ld_out + c) =
+                            make_uint2(pack2(__float_as_uint(s.x), __float_as_uint(s.y), g.type),
+                                       pack2(__float_as_uint(s.z), __float_as_uint(s.w), g.type));
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+        if (ch + 1 < chunks) fence_proxy_async_smem();            // the stages go back to TMA
+        __syncthreads();
+        tc_fence_after();
+    }
+    __syncwarp();
+    if (abort_flag && warp == 0 && lane == 0) { // drain what was sent before the shared memory goes away
+        for (int s = 0; s < stages && s < sent; ++s) {
+            const int last = (sent - 1 - s) / stages;             // the slot's last use
+            const uint64_t from = globaltimer_ns();
+            while (!mbar_try_wait(&full_bar[s], (uint32_t)(last & 1)) && globaltimer_ns() - from < kWaitLimitNs) {}
+        }
+        set_status(status, SF_STATUS_WAIT_TIMEOUT);
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, PN);
     }
 }
 
@@ -1234,21 +1497,25 @@ int launch(K kernel, int grid, int cluster, int threads, size_t smem, const GArg
 {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return SF_ERR_CUDA;
-    cudaLaunchAttribute attr[2];
-    // programmatic dependent launch: each kernel waits for its predecessor itself, behind what it can do without it
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr;
+    if (cluster > 1) {
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = cluster;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+    } else {
+        // programmatic dependent launch: the small kernels wait for their predecessor themselves, behind what they can
+        // do without it (4.4 -> 3.4 us for the smallest calls back to back)
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = as_stream(stream);
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kernel, g, status) != cudaSuccess) return SF_ERR_CUDA;
     return launch_status();
 }
@@ -1256,6 +1523,9 @@ int launch(K kernel, int grid, int cluster, int threads, size_t smem, const GArg
 // Pairs run when an expert has more than this many tokens on average.
 #ifndef SF_GROUPED_PAIR_FROM
 #define SF_GROUPED_PAIR_FROM 96
+#endif
+#ifndef SF_GROUPED_DW_OLD_BELOW
+#define SF_GROUPED_DW_OLD_BELOW 512
 #endif
 
 template <bool TRANS>
@@ -1338,10 +1608,14 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
     int rc = check_grouped(p, true);
     if (rc != SF_OK) return rc;
     if (accumulate && p->w_type != SF_TYPE_F32) return SF_ERR_ARG;
-    if (sm_count() <= 0) return SF_ERR_NO_DEVICE;
+    const int sms = sm_count();
+    if (sms <= 0) return SF_ERR_NO_DEVICE;
     GArgs g;
     memset(&g, 0, sizeof(g));
     g.offsets = p->offsets;
+    g.out = p->W;
+    g.ld_out = p->ld_w;
+    g.stride_out = p->E > 1 ? p->stride_w : 0;
     g.E = p->E;
     g.T = p->T;
     g.M = p->R;
@@ -1353,12 +1627,29 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
     const void *a = p->T > 0 ? p->A : p->W, *y = p->T > 0 ? p->Y : p->W;
     const int64_t ld_a = p->T > 0 ? p->ld_a : p->C, ld_y = p->T > 0 ? p->ld_y : p->R;
     const int64_t stride = p->E > 1 ? p->stride_w : (int64_t)p->R * p->ld_w;
-    if (!encode(&g.tm_w, p->type, a, p->C, p->T, ld_a, 0, 0, 64) || !encode(&g.tm_x, p->type, y, p->R, p->T, ld_y, 0, 0, 64) ||
-        !encode(&g.tm_out, p->w_type, p->W, p->C, p->R, p->ld_w, p->E, stride, 32))
+    auto tiles = [&](int rows, int cols) {
+        return (int64_t)((p->R + rows - 1) / rows) * ((p->C + cols - 1) / cols);
+    };
+    const int64_t busy = p->E < p->T ? p->E : p->T;      // experts with a token, at most
+    const int64_t pair_units = p->E * tiles(PM, PN);
+    if (busy * tiles(PM, PN) >= sms / 2) {
+        if (!encode(&g.tm_w, p->type, a, p->C, p->T, ld_a, 0, 0, 64) || !encode(&g.tm_x, p->type, y, p->R, p->T, ld_y, 0, 0, 64) ||
+            !encode(&g.tm_out, p->w_type, p->W, p->C, p->R, p->ld_w, p->E, stride, 32))
+            return SF_ERR_CUDA;
+        const int slots = pair_slots();
+        if (slots <= 0) return SF_ERR_CUDA;
+        const bool old = accumulate && p->T < (int64_t)SF_GROUPED_DW_OLD_BELOW * p->E;
+        return launch(old ? grouped_dw_kernel<true> : grouped_dw_kernel<false>,
+                      2 * (int)(pair_units < slots ? pair_units : slots), 2, W_THREADS, W_SMEM_BYTES, g, dev_status, stream);
+    }
+    // tokens in slices while that still leaves the units short of the device
+    int s = 1;
+    while (s < 4 && busy * tiles(SM_ROWS / s, PN / s) < 2 * sms && p->T > (int64_t)GK * s * p->E) s *= 2;
+    const int64_t units = p->E * tiles(SM_ROWS / s, PN / s);
+    g.stages = units <= sms ? 4 : 2;                     // one CTA to an SM, or two
+    if (!encode(&g.tm_w, p->type, a, p->C, p->T, ld_a, 0, 0, 64) ||
+        !encode(&g.tm_x, p->type, y, p->R, p->T, ld_y, 0, 0, 64, s == 4 ? 64 : 128))
         return SF_ERR_CUDA;
-    const int slots = pair_slots();
-    if (slots <= 0) return SF_ERR_CUDA;
-    const int64_t units = (int64_t)p->E * ((p->R + PM - 1) / PM) * ((p->C + 31) / 32);      // at most
-    return launch(grouped_dw_kernel, 2 * (int)(units < slots ? units : slots), 2, W_THREADS, W_SMEM_BYTES, g, dev_status,
-                  stream);
+    auto kernel = s == 1 ? grouped_dw_small_kernel<1> : s == 2 ? grouped_dw_small_kernel<2> : grouped_dw_small_kernel<4>;
+    return launch(kernel, (int)units, 1, D_THREADS, (size_t)g.stages * D_STAGE_BYTES + 1024, g, dev_status, stream);
 }

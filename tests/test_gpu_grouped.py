@@ -118,6 +118,22 @@ def test_dw(sf, counts, R, C, dt, out, add):
     assert int(status[0]) == 0
 
 
+@pytest.mark.parametrize("out,add", [(F32, False), (F32, True), (BF, False)])
+@pytest.mark.parametrize("counts,R,C", [([700, 301], 2056, 1544), ([1, 0, 1100, 960], 1288, 1800), ([2111], 2312, 2568),
+                                        ([64, 0, 961, 1025, 16], 1032, 1352)])
+def test_dw_of_many_tiles(sf, counts, R, C, out, add):
+    """Enough tokens and tiles for the pairs' kernel: whole and ragged last stages, empty experts, several chunks."""
+    test_dw(sf, counts, R, C, BF, out, add)
+
+
+@pytest.mark.parametrize("counts", [[5000], [3000, 0, 1999, 70]])
+@pytest.mark.parametrize("R,C", [(72, 136), (264, 200), (520, 712)])
+def test_dw_of_few_tiles_and_long_sums(sf, counts, R, C):
+    """Few tiles and many tokens: sums in slices, several chunks of each."""
+    test_dw(sf, counts, R, C, HF, F32, True)
+    test_dw(sf, counts, R, C, BF, BF, False)
+
+
 def strided(shape, dt, seed, pad, lead=0):
     """A view whose rows are pad elements further apart than they are long."""
     big = normal((*shape[:-1], shape[-1] + pad), dt, seed)
