@@ -78,7 +78,7 @@ struct GArgs {
     void *out;
     int64_t ld_out, stride_out;
     int32_t E, T, M, K, type;  // M: accumulator rows in all (forward R, dx C, dw R); K: forward C, dx R, dw C (its N)
-    int32_t nb, stages;              // single CTAs: token box, stages
+    int32_t nb, stages, rounds;      // single CTAs: token box, stages, whether a CTA may have several units
     int32_t out_f32, accumulate;     // dw
 };
 
@@ -520,56 +520,63 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 }
 
 // ------------------------------------------------------------------------------------------------
-// forward and dx, few tokens to an expert: a unit to a CTA, short sums
+// forward and dx, few tokens to an expert: single CTAs, two to an SM
 //
-// The time is that of the weights' way in, so what counts is that all SMs ask for them at once and early. With few
-// units, a unit is 128 / S accumulator rows and S slices of K: the M operand holds the same weight rows S times, slice
-// j of K in rows j * 128 / S .., the N operand the tokens S times, slice j in columns j * nb ... The products of one slice
-// with itself are the partial sums wanted; those of different slices are not read. S times the units, a S-th of the
-// steps, and no exchange between CTAs. (Splitting K over the CTAs of a cluster, which exchange partial sums through
-// distributed shared memory, took 63 us where this takes 27: 16 experts, 777 tokens, 2056 x 1416.)
+// The time is that of the weights' way in, so what counts is that all SMs ask for them at once, early and without a
+// pause: each CTA loads its next unit's weights while it multiplies and stores the one before. With few units, a unit is
+// 128 / S accumulator rows and S slices of K: the M operand holds the same weight rows S times, slice j of K in rows
+// j * 128 / S .., the N operand the tokens S times, slice j in columns j * nb ... The products of one slice with itself
+// are the partial sums wanted; those of different slices are not read. S times the units, a S-th of the steps, and no
+// exchange between CTAs. (Splitting K over the CTAs of a cluster, which exchange partial sums through distributed shared
+// memory, took 63 us where one slice took 27: 16 experts, 777 tokens, 2056 x 1416.)
 // ------------------------------------------------------------------------------------------------
 
 struct SUnit {
     int e, mt, t0, n;          // expert, tile of accumulator rows, first token, tokens; n = 0: no such unit
-    bool bad;                  // the offsets are not valid
 };
 
-// Unit u, found by each warp on its own from the offsets in shared memory (32 experts at a time).
-__device__ __forceinline__ SUnit small_unit(const GArgs &g, const int *off, int u, int m_tiles)
+// Unit u of a call that has a unit to a CTA at most, found by each warp on its own (32 experts at a time): the experts
+// are not ordered, and nothing is counted ahead.
+__device__ __forceinline__ SUnit scan_unit(const int *off, int E, int nb, int u, int m_tiles)
 {
     const int lane = threadIdx.x & 31;
     SUnit x;
     x.e = x.mt = x.t0 = x.n = 0;
     int run = 0;
-    bool bad = false;
-    for (int base = 0; base < g.E; base += 32) {
+    for (int base = 0; base < E && x.n == 0; base += 32) {
         const int e = base + lane;
-        int o0 = 0, o1 = 0;
-        if (e < g.E) {
-            o0 = off[e];
-            o1 = off[e + 1];
-        }
-        const bool wrong = o0 < 0 || o1 < o0 || o1 > g.T;
-        bad |= wrong;
-        const int cnt = wrong ? 0 : o1 - o0;
-        const int tile = cnt ? tile_tokens(cnt, g.nb, 16) : 16, tiles = cnt ? quot_up(cnt, tile) : 0;
+        const int o0 = e < E ? off[e] : 0, cnt = e < E ? off[e + 1] - o0 : 0;
+        const int tile = cnt ? tile_tokens(cnt, nb, 16) : 16, tiles = cnt ? quot_up(cnt, tile) : 0;
         const int units = tiles * m_tiles, inc = warp_inclusive_scan(units);
         const uint32_t past = __ballot_sync(0xffffffffu, run + inc > u);
-        if (past && x.n == 0) {
+        if (past) {
             const int l = __ffs(past) - 1;                   // the first expert whose units end behind u
             const int before = run + __shfl_sync(0xffffffffu, inc - units, l);
             const int first = __shfl_sync(0xffffffffu, o0, l), c = __shfl_sync(0xffffffffu, cnt, l);
             const int tl = __shfl_sync(0xffffffffu, tile, l), nt = __shfl_sync(0xffffffffu, tiles, l);
             x.e = base + l;
-            x.mt = quot(u - before, nt);                        // the tiles of one weight tile adjoin
+            x.mt = quot(u - before, nt);                     // the tiles of one weight tile adjoin
             const int t = u - before - x.mt * nt;
             x.t0 = first + t * tl;
             x.n = min(tl, c - t * tl);
         }
         run += __shfl_sync(0xffffffffu, inc, 31);
     }
-    x.bad = __any_sync(0xffffffffu, bad);
+    return x;
+}
+
+// The same from the plan.
+__device__ __forceinline__ SUnit plan_unit(const Plan &pl, int E, int nb, int u)
+{
+    SUnit x;
+    const int place = find_place(pl, E, u);
+    x.e = pl.order[place];
+    const int cnt = pl.off[x.e + 1] - pl.off[x.e];
+    const int tile = tile_tokens(cnt, nb, 16), nt = quot_up(cnt, tile);
+    x.mt = quot(u - pl.pre[place], nt);
+    const int t = u - pl.pre[place] - x.mt * nt;
+    x.t0 = pl.off[x.e] + t * tile;
+    x.n = min(tile, cnt - t * tile);
     return x;
 }
 
@@ -578,16 +585,17 @@ __global__ void __launch_bounds__(S_THREADS)
 grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full_bar[S_MAX_STAGES], empty_bar[S_MAX_STAGES], done_bar;
+    __shared__ uint64_t full_bar[S_MAX_STAGES], empty_bar[S_MAX_STAGES], tfull_bar[2], tempty_bar[2], drain_bar;
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile int abort_flag;
-    __shared__ int off[kMaxE + 1];
+    __shared__ Plan pl;
 
     constexpr int ROWS = SM_ROWS / S;           // accumulator rows of a unit
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nb = g.nb, stages = g.stages;
-    const int tmem_cols = S * nb < 32 ? 32 : S * nb;
+    const int buf_cols = S * nb;                // an accumulator; two where a CTA has several units
+    const int tmem_cols = max(32, g.rounds ? 2 * buf_cols : buf_cols);
 
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&g.tm_w);
@@ -597,56 +605,75 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
             mbar_init(&full_bar[s], 1);
             mbar_init(&empty_bar[s], 1);
         }
-        mbar_init(&done_bar, 1);
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&tfull_bar[a], 1);
+            mbar_init(&tempty_bar[a], S_EPI_WARPS);
+        }
+        mbar_init(&drain_bar, 1);
         fence_mbarrier_init();
     }
     if (warp == 1) tmem_alloc(&tmem_base_s, (uint32_t)tmem_cols);
     // What the launches before this one wrote is there from here on; the launch behind it may take what room is left.
     // (Not before the allocation: a successor that holds tensor memory while it waits would keep this CTA from it.)
     griddep_wait();
-    for (int e = tid; e <= g.E; e += S_THREADS) off[e] = g.offsets[e];
     tc_fence_before();
-    __syncthreads();
+    const bool valid = load_offsets(pl, g.offsets, g.E, g.T);
     tc_fence_after();
     griddep_launch_dependents();
-    const SUnit x = small_unit(g, off, blockIdx.x, (g.M + ROWS - 1) / ROWS);
     const uint32_t tmem_base = tmem_base_s;
-    if (x.bad || x.n == 0) {
-        if (x.bad && blockIdx.x == 0 && tid == 0) set_status(status, SF_STATUS_BAD_OFFSET);
-        __syncwarp();
-        if (warp == 1) tmem_dealloc(tmem_base, (uint32_t)tmem_cols);
-        return;
+    const int m_tiles = (g.M + ROWS - 1) / ROWS;
+    if (g.rounds && valid) {
+        order_experts(pl, g.E, [](int cnt) { return cnt; });
+        count_units(pl, g.E, [&](int cnt) { return cnt > 0 ? quot_up(cnt, tile_tokens(cnt, nb, 16)) * m_tiles : 0; });
     }
-    const int m0 = x.mt * ROWS;
     const int nk = ((g.K + GK - 1) / GK + S - 1) / S;          // steps of each slice (the last slice's may lie behind K: zeros)
     const int stage_bytes = S_W_BYTES + S * nb * GK * 2;
+    // this CTA's i-th unit
+    auto unit = [&](int i) {
+        SUnit x;
+        x.n = 0;
+        if (!valid) return x;
+        if (!g.rounds) return i == 0 ? scan_unit(pl.off, g.E, nb, blockIdx.x, m_tiles) : x;
+        const int u = blockIdx.x + i * gridDim.x;
+        return u < pl.pre[g.E] ? plan_unit(pl, g.E, nb, u) : x;
+    };
 
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0, sent = 0;
-            uint32_t phase = 0;
-            for (int i = 0; i < nk; ++i) {
-                if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag)) break;
-                uint8_t *sw = smem + stage * stage_bytes, *sx = sw + S_W_BYTES;
-                mbar_arrive_expect_tx(&full_bar[stage], stage_bytes);
+        // ------------------------------ TMA producer ------------------------------
+        int stage = 0, sent = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int r = 0; ok; ++r) {
+            const SUnit x = unit(r);
+            if (x.n == 0) break;
+            if (lane == 0) {
+                const int m0 = x.mt * ROWS;
+                for (int i = 0; i < nk; ++i) {
+                    if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag)) { ok = false; break; }
+                    uint8_t *sw = smem + stage * stage_bytes, *sx = sw + S_W_BYTES;
+                    mbar_arrive_expect_tx(&full_bar[stage], stage_bytes);
 #pragma unroll
-                for (int j = 0; j < S; ++j) {
-                    const int k = (j * nk + i) * GK;
-                    if (TRANS && S == 1) {
-                        tma_load_3d(sw, &g.tm_w, &full_bar[stage], m0, k, x.e);
-                        tma_load_3d(sw + G_BOX_BYTES, &g.tm_w, &full_bar[stage], m0 + 64, k, x.e);
-                    } else if (TRANS) {
-                        tma_load_3d(sw + j * (S_W_BYTES / S), &g.tm_w, &full_bar[stage], m0, k, x.e);
-                    } else {
-                        tma_load_3d(sw + j * (S_W_BYTES / S), &g.tm_w, &full_bar[stage], k, m0, x.e);
+                    for (int j = 0; j < S; ++j) {
+                        const int k = (j * nk + i) * GK;
+                        if (TRANS && S == 1) {
+                            tma_load_3d(sw, &g.tm_w, &full_bar[stage], m0, k, x.e);
+                            tma_load_3d(sw + G_BOX_BYTES, &g.tm_w, &full_bar[stage], m0 + 64, k, x.e);
+                        } else if (TRANS) {
+                            tma_load_3d(sw + j * (S_W_BYTES / S), &g.tm_w, &full_bar[stage], m0, k, x.e);
+                        } else {
+                            tma_load_3d(sw + j * (S_W_BYTES / S), &g.tm_w, &full_bar[stage], k, m0, x.e);
+                        }
+                        tma_load_2d(sx + j * nb * GK * 2, &g.tm_x, &full_bar[stage], k, x.t0);
                     }
-                    tma_load_2d(sx + j * nb * GK * 2, &g.tm_x, &full_bar[stage], k, x.t0);
+                    ++sent;
+                    if (++stage == stages) { stage = 0; phase ^= 1u; }
                 }
-                ++sent;
-                if (++stage == stages) { stage = 0; phase ^= 1u; }
             }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        if (lane == 0) {
             const uint64_t begin = globaltimer_ns();
-            while (!mbar_try_wait(&done_bar, 0) && globaltimer_ns() - begin < kWaitLimitNs) {}
+            while (!mbar_try_wait(&drain_bar, 0) && globaltimer_ns() - begin < kWaitLimitNs) {}
             if (abort_flag) {                   // drain what was sent before the shared memory goes away
                 for (int s = 0; s < stages && s < sent; ++s) {
                     const int last = (sent - 1 - s) / stages;        // the slot's last use
@@ -656,79 +683,106 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
             }
         }
     } else if (warp == 1) {
-        int stage = 0;
-        uint32_t phase = 0;
-        const uint32_t id = idesc(g.type, TRANS, false, S == 1 ? (x.n + 15) & ~15 : S * nb, SM_ROWS);
+        // ------------------------------ MMA issuer ------------------------------
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, buf_phase = 0;
+        bool ok = true;
         const uint32_t s0 = smem_u32(smem);
         // M-major weights of four slices lie in 32-column boxes with 64-byte rows, otherwise in 64-column boxes
         const uint64_t w0 = !TRANS ? kmajor(s0) : S == 4 ? mnmajor64(s0) : mnmajor(s0), x0 = kmajor(s0 + S_W_BYTES);
-        int i = 0;
-        for (; i < nk; ++i) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, &abort_flag))) break;
-            tc_fence_after();
-            const uint64_t dw = w0 + (uint64_t)(stage * (stage_bytes >> 4)), dx = x0 + (uint64_t)(stage * (stage_bytes >> 4));
-            if (elect_one()) {
+        for (int r = 0; ok; ++r) {
+            const SUnit x = unit(r);
+            if (x.n == 0) break;
+            const uint32_t id = idesc(g.type, TRANS, false, S == 1 ? (x.n + 15) & ~15 : S * nb, SM_ROWS);
+            const uint32_t d_tmem = tmem_base + (uint32_t)(buf * buf_cols);
+            ok = __all_sync(0xffffffffu, mbar_wait(&tempty_bar[buf], buf_phase ^ 1u, &abort_flag));
+            if (!ok) break;
+            for (int i = 0; i < nk; ++i) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, &abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t dw = w0 + (uint64_t)(stage * (stage_bytes >> 4)), dx = x0 + (uint64_t)(stage * (stage_bytes >> 4));
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < GK / G_UMMA_K; ++k)
-                    mma_bf16(tmem_base, dw + k * (!TRANS ? 2 : S == 4 ? 64 : 128), dx + k * 2, id, (i | k) != 0);
-                mma_commit(&empty_bar[stage]);
-                if (i == nk - 1) mma_commit(&done_bar);
+                    for (int k = 0; k < GK / G_UMMA_K; ++k)
+                        mma_bf16(d_tmem, dw + k * (!TRANS ? 2 : S == 4 ? 64 : 128), dx + k * 2, id, (i | k) != 0);
+                    mma_commit(&empty_bar[stage]);
+                    if (i == nk - 1) mma_commit(&tfull_bar[buf]);
+                }
+                __syncwarp();
+                if (++stage == stages) { stage = 0; phase ^= 1u; }
             }
-            __syncwarp();
-            if (++stage == stages) { stage = 0; phase ^= 1u; }
+            if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
         }
-        if (i < nk && elect_one()) mma_commit(&done_bar);     // gave up
+        if (elect_one()) mma_commit(&drain_bar);
+        __syncwarp();
+        const uint64_t begin = globaltimer_ns();
+        while (!mbar_try_wait(&drain_bar, 0) && globaltimer_ns() - begin < kWaitLimitNs) {}
+    } else {
+        // --------------------------- epilogue (warps 2..5) ---------------------------
+        const int quad = warp & 3;              // accumulator rows 32*quad .. 32*quad+31
+        const int slice = quad * S / 4;         // the slice they belong to
+        int buf = 0;
+        uint32_t buf_phase = 0;
+        for (int r = 0;; ++r) {
+            const SUnit x = unit(r);
+            if (x.n == 0) break;
+            const int m0 = x.mt * ROWS;
+            bool ready = mbar_wait(&tfull_bar[buf], buf_phase, &abort_flag);
+            ready = bar_all(1, 32 * S_EPI_WARPS, ready);     // the four warps go on together or not at all
+            if (!ready) break;
+            tc_fence_after();
+            uint16_t *out = static_cast<uint16_t *>(g.out) + (int64_t)x.t0 * g.ld_out;
+            const uint32_t t_row = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * buf_cols + slice * nb);
+            float *part = reinterpret_cast<float *>(smem);    // S > 1, [slice][token][row]: the stages are free, it is the only unit
+            for (int c = 0; c < x.n; c += 16) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(t_row + c, v);
+                tmem_ld_wait();
+                if (S == 1) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], g.type);
+                    store_tokens<16>(w, out + (int64_t)c * g.ld_out, g.ld_out, m0 + quad * 32 + lane, g.M, x.n - c);
+                } else {
+                    float *mine = part + (slice * nb + c) * ROWS + quad * 32 + lane - slice * ROWS;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) mine[j * ROWS] = __uint_as_float(v[j]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+            if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+            if (S > 1) {                        // the slices' sums, in their order; two rows of a token to a thread
+                bar_all(1, 32 * S_EPI_WARPS, true);
+                for (int i = tid - 64; i < x.n * (ROWS / 2); i += 32 * S_EPI_WARPS) {
+                    const int t = i / (ROWS / 2), row = 2 * (i - t * (ROWS / 2));
+                    float2 s = *reinterpret_cast<const float2 *>(part + t * ROWS + row);
+#pragma unroll
+                    for (int j = 1; j < S; ++j) {
+                        const float2 a = *reinterpret_cast<const float2 *>(part + (j * nb + t) * ROWS + row);
+                        s.x = __fadd_rn(s.x, a.x);
+                        s.y = __fadd_rn(s.y, a.y);
+                    }
+                    if (m0 + row < g.M)
+                        *reinterpret_cast<uint32_t *>(out + (int64_t)t * g.ld_out + m0 + row) =
+                            pack2(__float_as_uint(s.x), __float_as_uint(s.y), g.type);
+                }
+            }
+        }
     }
     __syncwarp();
-    // Everyone waits for the MMAs (the producer has, in lane 0).
-    if (!mbar_wait(&done_bar, 0, &abort_flag)) abort_flag = 1;
-    __syncthreads();
-    const bool ok = !abort_flag;
-    const int quad = warp & 3;
-    uint16_t *out = static_cast<uint16_t *>(g.out) + (int64_t)x.t0 * g.ld_out;
-    tc_fence_after();
-    const int slice = quad * S / 4;             // the slice that this warp's accumulator rows belong to
-    const uint32_t t_row = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(slice * nb);
-    float *part = reinterpret_cast<float *>(smem);            // [slice][token][row]: the stages are free
-    if (warp >= 2 && ok) {
-        for (int c = 0; c < x.n; c += 16) {
-            uint32_t v[16];
-            tmem_ld_32x32b_x16(t_row + c, v);
-            tmem_ld_wait();
-            if (S == 1) {
-                uint32_t w[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], g.type);
-                store_tokens<16>(w, out + (int64_t)c * g.ld_out, g.ld_out, m0 + quad * 32 + lane, g.M, x.n - c);
-            } else {
-                float *mine = part + (slice * nb + c) * ROWS + quad * 32 + lane - slice * ROWS;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) mine[j * ROWS] = __uint_as_float(v[j]);
-            }
-        }
-    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, (uint32_t)tmem_cols);
     }
-    if (S > 1 && ok) {                          // the slices' sums, in their order; two rows of a token to a thread
-        for (int i = tid; i < x.n * (ROWS / 2); i += S_THREADS) {
-            const int t = i / (ROWS / 2), r = 2 * (i - t * (ROWS / 2));
-            float2 s = *reinterpret_cast<const float2 *>(part + t * ROWS + r);
-#pragma unroll
-            for (int j = 1; j < S; ++j) {
-                const float2 a = *reinterpret_cast<const float2 *>(part + (j * nb + t) * ROWS + r);
-                s.x = __fadd_rn(s.x, a.x);
-                s.y = __fadd_rn(s.y, a.y);
-            }
-            if (m0 + r < g.M)
-                *reinterpret_cast<uint32_t *>(out + (int64_t)t * g.ld_out + m0 + r) =
-                    pack2(__float_as_uint(s.x), __float_as_uint(s.y), g.type);
-        }
+    if (tid == 0) {
+        if (abort_flag) set_status(status, SF_STATUS_WAIT_TIMEOUT);
+        if (!valid && blockIdx.x == 0) set_status(status, SF_STATUS_BAD_OFFSET);
     }
-    if (!ok && tid == 0) set_status(status, SF_STATUS_WAIT_TIMEOUT);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -1553,7 +1607,18 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
     const int w_rows = fwd ? 128 : 64;
     const int nk = (g.K + GK - 1) / GK;
 
-    if (p->T > (int64_t)SF_GROUPED_PAIR_FROM * p->E) {
+    // A token box that holds most experts in one tile: up to 32 tokens, where the weights outweigh the box, twice the
+    // average (a decode batch of 12 tokens each: 114.6 us against 116.5 with a box of 16), beyond that the average and
+    // a quarter (49 tokens each: 26.7 us with a box of 64, 31.0 with 128).
+    const int avg = (p->T + p->E - 1) / p->E;
+    int nb = 16;
+    while (nb < 128 && nb < p->T && 4 * nb < (nb < 32 ? 8 * avg : 5 * avg)) nb *= 2;
+    const int64_t busy = p->E < p->T ? p->E : p->T;      // experts with a token, at most
+    const int64_t tiles = busy + p->T / nb;              // token tiles, at most
+    const int64_t m_tiles = (g.M + SM_ROWS - 1) / SM_ROWS;
+    const bool one_round = tiles * m_tiles <= 2 * sms;
+
+    if (!one_round && p->T > (int64_t)SF_GROUPED_PAIR_FROM * p->E) {
         if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, w_rows) ||
             !encode(&g.tm_x, p->type, x, g.K, p->T, ld_x, 0, 0, 128))
             return SF_ERR_CUDA;
@@ -1563,29 +1628,25 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
         const int pairs = (int)(most < slots ? most : slots);
         return launch(grouped_pair_kernel<TRANS>, 2 * pairs, 2, P_THREADS, T_SMEM_BYTES, g, status, stream);
     }
-    // A token box that holds most experts in one tile: up to 32 tokens, where the weights outweigh the box, twice the
-    // average (a decode batch of 12 tokens each: 114.6 us against 116.5 with a box of 16), beyond that the average and
-    // a quarter (49 tokens each: 26.7 us with a box of 64, 31.0 with 128).
-    const int avg = (p->T + p->E - 1) / p->E;
-    int nb = 16;
-    while (nb < 128 && nb < p->T && 4 * nb < (nb < 32 ? 8 * avg : 5 * avg)) nb *= 2;
-    const int64_t busy = p->E < p->T ? p->E : p->T;      // experts with a token, at most
-    const int64_t m_tiles = (g.M + SM_ROWS - 1) / SM_ROWS;
-    // K in slices while the units still fit the device at once, two CTAs to an SM
+    // K in slices while an expert's tokens fit one tile and the units fit the device at once, two CTAs to an SM
     int s = 1;
-    while (s < 4 && busy * m_tiles * 2 * s <= 2 * sms && nk >= 4 * s && 2 * s * nb <= 256) s *= 2;
+    while (s < 4 && avg <= nb && busy * m_tiles * 2 * s <= 2 * sms && nk >= 4 * s && 2 * s * nb <= 256) s *= 2;
     g.nb = nb;
+    // Several units to a CTA, planned ahead, where a unit is short (64 experts of 1024 x 1024 over 64 tokens each: 35.6 ->
+    // 32.1 us); long ones come out more even as a CTA each (the decode batch above: 114.6 against 117.5 us).
+    g.rounds = s == 1 && tiles * m_tiles > 2 * sms && nk <= 24;
     const int stage_bytes = S_W_BYTES + s * nb * GK * 2;
     g.stages = 100 * 1024 / stage_bytes;
     if (g.stages > S_MAX_STAGES) g.stages = S_MAX_STAGES;
     const int rows = SM_ROWS / s;
-    const int64_t units = (busy + p->T / nb) * ((g.M + rows - 1) / rows);          // at most
+    const int64_t units = tiles * ((g.M + rows - 1) / rows);                       // at most
     const int box_rows = fwd ? rows : 64, box_bytes = !fwd && s == 4 ? 64 : 128;
     if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, box_rows, box_bytes) ||
         !encode(&g.tm_x, p->type, x, g.K, p->T, ld_x, 0, 0, nb))
         return SF_ERR_CUDA;
     auto kernel = s == 1 ? grouped_small_kernel<TRANS, 1> : s == 2 ? grouped_small_kernel<TRANS, 2> : grouped_small_kernel<TRANS, 4>;
-    return launch(kernel, (int)units, 1, S_THREADS, (size_t)g.stages * stage_bytes + 1024, g, status, stream);
+    const int grid = (int)(g.rounds ? 2 * sms : units);
+    return launch(kernel, grid, 1, S_THREADS, (size_t)g.stages * stage_bytes + 1024, g, status, stream);
 }
 
 }  // namespace
@@ -1632,7 +1693,10 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
     };
     const int64_t busy = p->E < p->T ? p->E : p->T;      // experts with a token, at most
     const int64_t pair_units = p->E * tiles(PM, PN);
-    if (busy * tiles(PM, PN) >= sms / 2) {
+    // Pairs, unless they would be few, or one round of single CTAs does it all with short sums (8 experts of 1024 x 1024
+    // over 128 tokens each: 11.1 us against 13.1; one of 2048 x 2048 over 4,096: 56 us against 30).
+    const bool one_round = busy * tiles(SM_ROWS, PN) <= 2 * sms && p->T <= (int64_t)512 * p->E;
+    if (busy * tiles(PM, PN) >= sms / 4 && !one_round) {
         if (!encode(&g.tm_w, p->type, a, p->C, p->T, ld_a, 0, 0, 64) || !encode(&g.tm_x, p->type, y, p->R, p->T, ld_y, 0, 0, 64) ||
             !encode(&g.tm_out, p->w_type, p->W, p->C, p->R, p->ld_w, p->E, stride, 32))
             return SF_ERR_CUDA;
@@ -1642,9 +1706,10 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
         return launch(old ? grouped_dw_kernel<true> : grouped_dw_kernel<false>,
                       2 * (int)(pair_units < slots ? pair_units : slots), 2, W_THREADS, W_SMEM_BYTES, g, dev_status, stream);
     }
-    // tokens in slices while that still leaves the units short of the device
+    // Tokens in slices while the units still fit the device at once (one expert of 512 x 512 over 8,192 tokens: 102, 43 and
+    // 24 us with 1, 2 and 4 slices; where they do not fit, every slice more costs its share of the loads again).
     int s = 1;
-    while (s < 4 && busy * tiles(SM_ROWS / s, PN / s) < 2 * sms && p->T > (int64_t)GK * s * p->E) s *= 2;
+    while (s < 4 && busy * tiles(SM_ROWS / (2 * s), PN / (2 * s)) <= 2 * sms && p->T > (int64_t)GK * s * p->E) s *= 2;
     const int64_t units = p->E * tiles(SM_ROWS / s, PN / s);
     g.stages = units <= sms ? 4 : 2;                     // one CTA to an SM, or two
     if (!encode(&g.tm_w, p->type, a, p->C, p->T, ld_a, 0, 0, 64) ||
