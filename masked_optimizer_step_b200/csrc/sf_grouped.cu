@@ -78,7 +78,7 @@ struct GArgs {
     void *out;
     int64_t ld_out, stride_out;
     int32_t E, T, M, K, type;  // M: accumulator rows in all (forward R, dx C, dw R); K: forward C, dx R, dw C (its N)
-    int32_t nb, stages, rounds;      // single CTAs: token box, stages, whether a CTA may have several units
+    int32_t nb, stages;              // single CTAs: token box, stages
     int32_t out_f32, accumulate;     // dw
 };
 
@@ -580,7 +580,8 @@ __device__ __forceinline__ SUnit plan_unit(const Plan &pl, int E, int nb, int u)
     return x;
 }
 
-template <bool TRANS, int S>
+// ROUNDS: a CTA may have several units.
+template <bool TRANS, int S, bool ROUNDS>
 __global__ void __launch_bounds__(S_THREADS)
 grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 {
@@ -595,7 +596,7 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nb = g.nb, stages = g.stages;
     const int buf_cols = S * nb;                // an accumulator; two where a CTA has several units
-    const int tmem_cols = max(32, g.rounds ? 2 * buf_cols : buf_cols);
+    const int tmem_cols = max(32, ROUNDS ? 2 * buf_cols : buf_cols);
 
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&g.tm_w);
@@ -613,29 +614,28 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         fence_mbarrier_init();
     }
     if (warp == 1) tmem_alloc(&tmem_base_s, (uint32_t)tmem_cols);
-    // What the launches before this one wrote is there from here on; the launch behind it may take what room is left.
-    // (Not before the allocation: a successor that holds tensor memory while it waits would keep this CTA from it.)
-    griddep_wait();
+    griddep_wait();                             // what the launches before this one wrote is there from here on
     tc_fence_before();
     const bool valid = load_offsets(pl, g.offsets, g.E, g.T);
     tc_fence_after();
-    griddep_launch_dependents();
     const uint32_t tmem_base = tmem_base_s;
     const int m_tiles = (g.M + ROWS - 1) / ROWS;
-    if (g.rounds && valid) {
+    if (ROUNDS && valid) {
         order_experts(pl, g.E, [](int cnt) { return cnt; });
         count_units(pl, g.E, [&](int cnt) { return cnt > 0 ? quot_up(cnt, tile_tokens(cnt, nb, 16)) * m_tiles : 0; });
     }
     const int nk = ((g.K + GK - 1) / GK + S - 1) / S;          // steps of each slice (the last slice's may lie behind K: zeros)
     const int stage_bytes = S_W_BYTES + S * nb * GK * 2;
     // this CTA's i-th unit
+    SUnit only;
+    only.n = 0;
+    if (!ROUNDS && valid) only = scan_unit(pl.off, g.E, nb, blockIdx.x, m_tiles);
     auto unit = [&](int i) {
         SUnit x;
         x.n = 0;
-        if (!valid) return x;
-        if (!g.rounds) return i == 0 ? scan_unit(pl.off, g.E, nb, blockIdx.x, m_tiles) : x;
+        if (!ROUNDS) return i == 0 ? only : x;
         const int u = blockIdx.x + i * gridDim.x;
-        return u < pl.pre[g.E] ? plan_unit(pl, g.E, nb, u) : x;
+        return valid && u < pl.pre[g.E] ? plan_unit(pl, g.E, nb, u) : x;
     };
 
     if (warp == 0) {
@@ -672,6 +672,9 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
             ok = __shfl_sync(0xffffffffu, ok, 0);
         }
         if (lane == 0) {
+            // The launch behind this one may take what room is left: now, when this CTA's time is nearly up (any sooner, its
+            // CTAs crowd the SMs that this launch left room on: 8 experts of 1024 x 1024, 512 tokens: 11.1 us against 9.4).
+            griddep_launch_dependents();
             const uint64_t begin = globaltimer_ns();
             while (!mbar_try_wait(&drain_bar, 0) && globaltimer_ns() - begin < kWaitLimitNs) {}
             if (abort_flag) {                   // drain what was sent before the shared memory goes away
@@ -1223,7 +1226,6 @@ grouped_dw_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
     tc_fence_before();
     bad = __syncthreads_or(bad);
     tc_fence_after();
-    griddep_launch_dependents();
     const uint32_t tmem_base = tmem_base_s;
 
     const int n_tiles = (g.K + COLS - 1) / COLS, per = (g.M + ROWS - 1) / ROWS * n_tiles;
@@ -1281,6 +1283,7 @@ grouped_dw_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                     ++sent;
                     if (++stage == stages) { stage = 0; phase ^= 1u; }
                 }
+                if (end == nk) griddep_launch_dependents();
                 const uint64_t from = globaltimer_ns();
                 while (!mbar_try_wait(&done_bar, (uint32_t)(ch & 1)) && globaltimer_ns() - from < kWaitLimitNs) {}
             }
@@ -1634,7 +1637,7 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
     g.nb = nb;
     // Several units to a CTA, planned ahead, where a unit is short (64 experts of 1024 x 1024 over 64 tokens each: 35.6 ->
     // 32.1 us); long ones come out more even as a CTA each (the decode batch above: 114.6 against 117.5 us).
-    g.rounds = s == 1 && tiles * m_tiles > 2 * sms && nk <= 24;
+    const bool rounds = s == 1 && tiles * m_tiles > 2 * sms && nk <= 24;
     const int stage_bytes = S_W_BYTES + s * nb * GK * 2;
     g.stages = 100 * 1024 / stage_bytes;
     if (g.stages > S_MAX_STAGES) g.stages = S_MAX_STAGES;
@@ -1644,8 +1647,9 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
     if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, box_rows, box_bytes) ||
         !encode(&g.tm_x, p->type, x, g.K, p->T, ld_x, 0, 0, nb))
         return SF_ERR_CUDA;
-    auto kernel = s == 1 ? grouped_small_kernel<TRANS, 1> : s == 2 ? grouped_small_kernel<TRANS, 2> : grouped_small_kernel<TRANS, 4>;
-    const int grid = (int)(g.rounds ? 2 * sms : units);
+    auto kernel = rounds ? grouped_small_kernel<TRANS, 1, true> : s == 1 ? grouped_small_kernel<TRANS, 1, false>
+                  : s == 2 ? grouped_small_kernel<TRANS, 2, false> : grouped_small_kernel<TRANS, 4, false>;
+    const int grid = (int)(rounds ? 2 * sms : units);
     return launch(kernel, grid, 1, S_THREADS, (size_t)g.stages * stage_bytes + 1024, g, status, stream);
 }
 
