@@ -381,7 +381,7 @@ int sf_masked_dw_phase(const sf_dw_problem *probs /* host [n] */, int n, void *w
  * biases, heads, adapters, experts' weights) take a dense AdamW step. A call takes any number of
  * tensors of any lengths at once.
  * Per element, with f = factor[1] (1 when factor is NULL), t = step[0] + 1 and every operation
- * rounded in fp32:
+ * rounded in fp32 (the quotient is within 2 units in the last place):
  *   g  = clamp(grad * f, -clip, clip)                   (clip <= 0: no clamp)
  *   m1 = beta1 * m + one_minus_b1 * g,   v1 = beta2 * v + one_minus_b2 * g * g
  *   u  = (m1 * bc1[t]) / (sqrt(v1) * sqrt(bc2[t]) + eps)
@@ -412,7 +412,8 @@ int sf_masked_dw_phase(const sf_dw_problem *probs /* host [n] */, int n, void *w
  *
  * Requirements: n >= 0; p, g, m, v, live 16-byte aligned; p fp32 or bf16; g fp32, bf16 or fp16;
  * m_scale, v_scale present for 8-bit moments. Buffers of one call must not overlap.
- * Launches: one per 384 non-empty tensors. Errors: SF_ERR_ARG, SF_ERR_ALIGN.
+ * Launches: one per 384 non-empty tensors; the step's tensors with fp32 and with 8-bit moments are
+ * launched apart. Errors: SF_ERR_ARG, SF_ERR_ALIGN, SF_ERR_UNSUPPORTED (over 2^40 elements).
  */
 #define SF_DENSE_BLOCK 256
 #define SF_DENSE_PER_LAUNCH 384

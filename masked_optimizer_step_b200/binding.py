@@ -457,12 +457,19 @@ def _type(t, allowed, what) -> int:
     return k
 
 
-def _one_device(*tensors):
-    """The index of the device that all the given tensors (None among them) are on."""
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1 or next(iter(devs)).type != "cuda":
+def _one_device(*tensors) -> int:
+    """The index of the GPU that all the given tensors (None among them) are on."""
+    index = -1
+    for t in tensors:
+        if t is None:
+            continue
+        d = t.get_device()
+        if d < 0 or (index >= 0 and d != index):
+            raise ValueError("device tensors on one GPU expected")
+        index = d
+    if index < 0:
         raise ValueError("device tensors on one GPU expected")
-    return next(iter(devs)).index
+    return index
 
 
 def _on_current(index: int):
@@ -528,8 +535,9 @@ class DenseTensors:
         self.descs = [t.desc() if isinstance(t, Dense) else t for t in tensors]
         self.n = len(self.descs)
         self.arr = (sf_dense * max(self.n, 1))(*[d.c for d in self.descs])
-        refs = [t for d in self.descs for t in d.refs]
-        self.device = _one_device(*refs) if self.n else None
+        self.anchor = self.descs[0].refs[0] if self.n else None
+        if self.n:
+            _one_device(*[t for d in self.descs for t in d.refs])
 
 
 def step_words(device=None) -> torch.Tensor:
@@ -542,28 +550,26 @@ def grad_norm_workspace(tensors: DenseTensors, device="cuda") -> torch.Tensor:
     return torch.zeros(load().sf_grad_norm_ws_bytes(tensors.arr, tensors.n), dtype=torch.uint8, device=device)
 
 
-def _check_words(name, t, dtype, device):
+def _check_words(name, t, dtype):
     if t.dtype != dtype or t.numel() < 2 or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous tensor of two {dtype} expected")
-    if device is not None and t.device.index != device:
-        raise ValueError(f"{name} is on another device than the tensors")
 
 
 def sf_grad_norm(tensors: DenseTensors, out, ws, max_norm: float = 0.0, inv_scale: float = 1.0, status=None,
                  stream=None):
     """out (two floats): the gradients' global norm and the factor that clips it, for sf_adamw_step."""
-    _check_words("out", out, torch.float32, tensors.device)
-    _on_current(_one_device(out, ws, status))
+    _check_words("out", out, torch.float32)
+    _on_current(_one_device(tensors.anchor, out, ws, status))
     _check(load().sf_grad_norm(tensors.arr, tensors.n, inv_scale, max_norm, _ptr(out), _ptr(ws),
                                ws.numel() * ws.element_size(), _ptr(status), _stream(stream)), "sf_grad_norm")
 
 
 def sf_adamw_step(tensors: DenseTensors, hp: AdamParams, step, factor=None, status=None, stream=None):
     """One AdamW step of every tensor; step: step_words(), factor: sf_grad_norm's output or None."""
-    _check_words("step", step, torch.int32, tensors.device)
+    _check_words("step", step, torch.int32)
     if factor is not None:
-        _check_words("factor", factor, torch.float32, tensors.device)
-    _on_current(_one_device(step, factor, status, hp.bc1))
+        _check_words("factor", factor, torch.float32)
+    _on_current(_one_device(tensors.anchor, step, factor, status, hp.bc1))
     h = hp.struct()
     _check(load().sf_adamw_step(tensors.arr, tensors.n, ctypes.byref(h), _ptr(step), _ptr(factor), _ptr(status),
                                 _stream(stream)), "sf_adamw_step")
@@ -604,7 +610,7 @@ def grouped_problem(A, W, Y, offsets) -> Desc:
 
 
 def _grouped(name, p: Desc, status, stream, *extra):
-    _on_current(p.refs[1].device.index)
+    _on_current(_one_device(p.refs[1], status))
     _check(getattr(load(), name)(ctypes.byref(p.c), *extra, _ptr(status), _stream(stream)), name)
 
 

@@ -37,15 +37,19 @@ struct DenseDesc {
     float *m_scale, *v_scale;
     uint16_t *live;
     float decay;
-    int32_t unit_begin;                       // units of the tensors before this one
     uint8_t p_type, g_type, state_type, pad;
 };
 
+// The tensors of a launch, as kernel parameters: a launch carries all of them, so there is a form for few, one for some
+// and one for many (65 tensors: 13 us from call to call with 384 places, 8 with 96).
+template <int N>
 struct DenseBatch {
     int32_t n, units, per;                    // tensors, units in all, blocks of a unit per warp
-    DenseDesc d[kMaxTensors];
+    int32_t unit_begin[N];                    // units of the tensors before this one
+    DenseDesc d[N];
 };
-static_assert(sizeof(DenseBatch) <= 32000, "kernel parameter space");
+static_assert(sizeof(DenseBatch<kMaxTensors>) <= 32000, "kernel parameter space");
+constexpr int kFew = 16, kSome = 96;
 
 struct StepArgs {
     float beta1, beta2, omb1, omb2, eps, lr, wd, clip;
@@ -55,42 +59,57 @@ struct StepArgs {
     const float *factor;
 };
 
-__device__ __forceinline__ int find_tensor(const DenseBatch &b, int unit)
+template <int N>
+__device__ __forceinline__ int find_tensor(const DenseBatch<N> &b, int unit)
 {
     int lo = 0, hi = b.n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (b.d[mid].unit_begin <= unit) lo = mid; else hi = mid - 1;
+        if (b.unit_begin[mid] <= unit) lo = mid; else hi = mid - 1;
     }
     return lo;
 }
 
-// Up to eight consecutive elements at `at` as fp32 (the first `cnt`; the rest are zero).
-__device__ __forceinline__ void load8(float (&x)[8], const void *base, int type, int64_t at, int cnt)
+// A lane's eight consecutive elements as they lie in memory: 16 bytes of 16-bit values, 32 of fp32. The first `cnt` are
+// loaded, the rest are zero.
+struct Raw8 {
+    uint4 a, b;
+};
+
+__device__ __forceinline__ Raw8 load_raw(const void *base, int type, int64_t at, int cnt)
+{
+    Raw8 r;
+    r.a = r.b = make_uint4(0u, 0u, 0u, 0u);
+    if (type == SF_TYPE_F32) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + at);
+        if (cnt == 8) {
+            r.a = __ldcs(src);
+            r.b = __ldcs(src + 1);
+        } else if (cnt > 0) {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(src);
+            r.a = make_uint4(w[0], cnt > 1 ? w[1] : 0u, cnt > 2 ? w[2] : 0u, cnt > 3 ? w[3] : 0u);
+            r.b = make_uint4(cnt > 4 ? w[4] : 0u, cnt > 5 ? w[5] : 0u, cnt > 6 ? w[6] : 0u, 0u);
+        }
+    } else {
+        const uint16_t *src = static_cast<const uint16_t *>(base) + at;
+        if (cnt == 8) {
+            r.a = __ldcs(reinterpret_cast<const uint4 *>(src));
+        } else if (cnt > 0) {
+            auto pair = [&](int e) { return (e < cnt ? (uint32_t)src[e] : 0u) | (e + 1 < cnt ? (uint32_t)src[e + 1] << 16 : 0u); };
+            r.a = make_uint4(pair(0), pair(2), pair(4), pair(6));
+        }
+    }
+    return r;
+}
+
+__device__ __forceinline__ void to_float(float (&x)[8], const Raw8 &r, int type)
 {
     if (type == SF_TYPE_F32) {
-        const float *src = static_cast<const float *>(base) + at;
-        if (cnt == 8) {
-            const float4 a = __ldcs(reinterpret_cast<const float4 *>(src));
-            const float4 c = __ldcs(reinterpret_cast<const float4 *>(src) + 1);
-            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-            x[4] = c.x; x[5] = c.y; x[6] = c.z; x[7] = c.w;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = e < cnt ? src[e] : 0.0f;
-        }
+        x[0] = __uint_as_float(r.a.x); x[1] = __uint_as_float(r.a.y); x[2] = __uint_as_float(r.a.z); x[3] = __uint_as_float(r.a.w);
+        x[4] = __uint_as_float(r.b.x); x[5] = __uint_as_float(r.b.y); x[6] = __uint_as_float(r.b.z); x[7] = __uint_as_float(r.b.w);
         return;
     }
-    const uint16_t *src = static_cast<const uint16_t *>(base) + at;
-    uint32_t w[4];
-    if (cnt == 8) {
-        const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(src));
-        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            w[e] = (2 * e < cnt ? (uint32_t)src[2 * e] : 0u) | (2 * e + 1 < cnt ? (uint32_t)src[2 * e + 1] << 16 : 0u);
-    }
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if (type == SF_TYPE_BF16) {
@@ -157,14 +176,15 @@ __device__ __forceinline__ void decode8(float (&x)[8], uint2 codes, float scale)
     }
 }
 
-// Codes and scale of a block's values (this lane's eight); POSITIVE values keep a positive code.
+// Codes and scale of a block's values (this lane's eight); returns the scale. POSITIVE: no value is negative, and a value
+// above zero keeps a code above zero.
 template <bool POSITIVE>
-__device__ __forceinline__ void encode8(const float (&x)[8], void *base, int64_t at, int cnt, float *scale, int lane)
+__device__ __forceinline__ float encode8(const float (&x)[8], void *base, int64_t at, int cnt, float *scale, int lane)
 {
-    uint32_t big = 0;
+    uint32_t big = 0;                                // magnitudes order as their bits; a NaN is the largest
 #pragma unroll
-    for (int e = 0; e < 8; ++e) big = max(big, __float_as_uint(fabsf(x[e])));
-    big = __reduce_max_sync(0xffffffffu, big);       // magnitudes order as their bits; a NaN is the largest
+    for (int e = 0; e < 8; ++e) big = max(big, POSITIVE ? __float_as_uint(x[e]) : __float_as_uint(x[e]) & 0x7FFFFFFFu);
+    big = __reduce_max_sync(0xffffffffu, big);
     float sc = __fmul_rn(__uint_as_float(big), 1.0f / 448.0f);
     if (sc < kScaleFloor) sc = kScaleFloor;          // a NaN stays
     const float inv = __frcp_rn(sc);
@@ -173,8 +193,8 @@ __device__ __forceinline__ void encode8(const float (&x)[8], void *base, int64_t
     for (int e = 0; e < 4; ++e) {
         float a = __fmul_rn(x[2 * e], inv), b = __fmul_rn(x[2 * e + 1], inv);
         if (POSITIVE) {
-            if (x[2 * e] > 0.0f && a < kSmallestCode) a = kSmallestCode;
-            if (x[2 * e + 1] > 0.0f && b < kSmallestCode) b = kSmallestCode;
+            if (x[2 * e] > 0.0f) a = fmaxf(a, kSmallestCode);
+            if (x[2 * e + 1] > 0.0f) b = fmaxf(b, kSmallestCode);
         }
         w[e >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) << (16 * (e & 1));
     }
@@ -187,12 +207,84 @@ __device__ __forceinline__ void encode8(const float (&x)[8], void *base, int64_t
             if (e < cnt) dst[e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
     }
     if (lane == 0) *scale = sc;
+    return sc;
 }
 
-__global__ void __launch_bounds__(kThreads)
-adamw_kernel(const __grid_constant__ DenseBatch b, const StepArgs a, uint32_t *status)
+// A warp's way through the blocks of its CTA's units.
+template <int N>
+struct Cursor {
+    const DenseBatch<N> &b;
+    int unit, which, k;        // unit, its tensor, block of the unit
+    int64_t blk;               // block of the tensor
+
+    __device__ __forceinline__ Cursor(const DenseBatch<N> &batch) : b(batch), unit((int)blockIdx.x - (int)gridDim.x), which(0), k(batch.per), blk(0)
+    {
+        next();
+    }
+    __device__ __forceinline__ bool there() const { return unit < b.units; }
+    __device__ __forceinline__ void next()
+    {
+        ++k;
+        blk += kWarps;
+        while (k >= b.per || blk * kBlock >= b.d[which].n) {
+            unit += gridDim.x;
+            if (unit >= b.units) return;
+            which = find_tensor(b, unit);
+            k = 0;
+            blk = (int64_t)(unit - b.unit_begin[which]) * b.per * kWarps + (threadIdx.x >> 5);
+        }
+    }
+};
+
+// What a block's step reads, as it lies in memory.
+template <bool CODED>
+struct Block {
+    Raw8 p, g, m, v;           // moments: fp32
+    uint2 cm, cv;              // or codes
+    float sm, sv;              // and their scales
+
+    __device__ __forceinline__ void load(const DenseDesc &d, int64_t blk, int lane)
+    {
+        const int64_t at = blk * kBlock + lane * kLaneElems;
+        const int cnt = (int)max((int64_t)0, min((int64_t)8, d.n - at));
+        p = load_raw(d.p, d.p_type, at, cnt);
+        g = load_raw(d.g, d.g_type, at, cnt);
+        if (CODED) {
+            cm = load8_codes(d.m, at, cnt);
+            cv = load8_codes(d.v, at, cnt);
+            sm = d.m_scale[blk];
+            sv = d.v_scale[blk];
+        } else {
+            m = load_raw(d.m, SF_TYPE_F32, at, cnt);
+            v = load_raw(d.v, SF_TYPE_F32, at, cnt);
+        }
+    }
+};
+
+// The lines of block `blk` into L2, ahead of its loads: a lane to a line of 128 bytes, 8 for an array of 32-bit values,
+// 4 of 16, 2 of 8.
+__device__ __forceinline__ void prefetch_block(const DenseDesc &d, int64_t blk, int lane)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int p_size = d.p_type == SF_TYPE_F32 ? 4 : 2, g_size = d.g_type == SF_TYPE_F32 ? 4 : 2;
+    const char *base = static_cast<const char *>(lane < 8 ? d.p : lane < 16 ? d.g : lane < 24 ? d.m : d.v);
+    const int size = lane < 8 ? p_size : lane < 16 ? g_size : 1, line = lane & 7;
+    const int64_t off = blk * kBlock * size + line * 128;
+    if (line < 2 * size && off < d.n * size) prefetch_l2(base + off);
+}
+
+// With fp32 moments a block's loads (3.5 KB a warp) are issued behind the stores of the block before, in registers: 900 us
+// for a 7B-shaped layer, 6.3 TB/s. With 8-bit moments they are 2 KB and the arithmetic takes about as long as the memory
+// (a correctly rounded quotient in place of the approximate one costs 6%), so a block is loaded where it is used, the
+// next one is asked for in L2 before that, and four CTAs to an SM hide one another's waits.
+template <int N, bool CODED>
+__global__ void __launch_bounds__(kThreads, CODED ? 4 : 3)
+adamw_kernel(const __grid_constant__ DenseBatch<N> b, const StepArgs a, uint32_t *status)
+{
+    const int lane = threadIdx.x & 31;
+    Cursor<N> at(b);
+    Block<CODED> cur;
+    if (!CODED && at.there()) cur.load(b.d[at.which], at.blk, lane);     // before the step's own words: two trips to memory
+    if (CODED && at.there()) prefetch_block(b.d[at.which], at.blk, lane);
     const int t = a.step[0] + 1;
     const float f = a.factor ? a.factor[1] : 1.0f;
     if (!(f != 0.0f) || f != f) {                    // the gradient was not finite: leave everything
@@ -203,51 +295,60 @@ adamw_kernel(const __grid_constant__ DenseBatch b, const StepArgs a, uint32_t *s
     const float bc1 = a.bc1[ti], root2 = __fsqrt_rn(a.bc2[ti]);
     float nan_sum = 0.0f;                            // stays 0 while everything is finite
 
-    for (int unit = blockIdx.x; unit < b.units; unit += gridDim.x) {
-        const DenseDesc &d = b.d[find_tensor(b, unit)];
-        const int64_t first = (int64_t)(unit - d.unit_begin) * b.per * kWarps;     // the unit's first block
+    while (at.there()) {
+        const DenseDesc &d = b.d[at.which];
+        const int64_t blk = at.blk, first = blk * kBlock + lane * kLaneElems;
+        const int cnt = (int)max((int64_t)0, min((int64_t)8, d.n - first));
+        if (CODED) cur.load(d, blk, lane);
+        at.next();
+        if (CODED && at.there()) prefetch_block(b.d[at.which], at.blk, lane);
+        float p[8], g[8], m[8], v[8];
+        to_float(p, cur.p, d.p_type);
+        to_float(g, cur.g, d.g_type);
+        if (CODED) {
+            decode8(m, cur.cm, cur.sm);
+            decode8(v, cur.cv, cur.sv);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], v[e]);
+        } else {
+            to_float(m, cur.m, SF_TYPE_F32);
+            to_float(v, cur.v, SF_TYPE_F32);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], f);
+        if (a.clip > 0.0f) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = fminf(fmaxf(g[e], -a.clip), a.clip);
+        }
         const float wd = __fmul_rn(d.decay, __fmul_rn(a.lr, a.wd));
-        for (int k = 0; k < b.per; ++k) {
-            const int64_t blk = first + (int64_t)k * kWarps + warp;
-            const int64_t at = blk * kBlock + lane * kLaneElems;
-            if (blk * kBlock >= d.n) break;
-            const int cnt = (int)max((int64_t)0, min((int64_t)8, d.n - at));
-            float p[8], g[8], m[8], v[8];
-            const bool coded = d.state_type == SF_TYPE_E4M3;
-            load8(p, d.p, d.p_type, at, cnt);
-            load8(g, d.g, d.g_type, at, cnt);
-            if (coded) {
-                const uint2 cm = load8_codes(d.m, at, cnt), cv = load8_codes(d.v, at, cnt);
-                decode8(m, cm, d.m_scale[blk]);
-                decode8(v, cv, d.v_scale[blk]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], v[e]);
-            } else {
-                load8(m, d.m, SF_TYPE_F32, at, cnt);
-                load8(v, d.v, SF_TYPE_F32, at, cnt);
-            }
+        for (int e = 0; e < 8; ++e) {
+            m[e] = __fadd_rn(__fmul_rn(m[e], a.beta1), __fmul_rn(g[e], a.omb1));
+            v[e] = __fadd_rn(__fmul_rn(v[e], a.beta2), __fmul_rn(__fmul_rn(g[e], g[e]), a.omb2));
+            const float root = __fsqrt_rn(v[e]);
+            const float u = __fdividef(__fmul_rn(m[e], bc1), __fmaf_rn(root, root2, a.eps));
+            p[e] = __fmaf_rn(-wd, p[e], __fmaf_rn(-a.lr, u, p[e]));
+            if (!CODED && e < cnt) nan_sum = __fmaf_rn(v[e], 0.0f, nan_sum);
+            if (CODED) v[e] = root;
+        }
+        if (cnt == 8) {                              // elements behind the end are not looked at
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float x = __fmul_rn(g[e], f);
-                if (a.clip > 0.0f) x = fminf(fmaxf(x, -a.clip), a.clip);
-                m[e] = __fadd_rn(__fmul_rn(m[e], a.beta1), __fmul_rn(x, a.omb1));
-                v[e] = __fadd_rn(__fmul_rn(v[e], a.beta2), __fmul_rn(__fmul_rn(x, x), a.omb2));
-                const float root = __fsqrt_rn(v[e]);
-                const float u = __fdiv_rn(__fmul_rn(m[e], bc1), __fmaf_rn(root, root2, a.eps));
-                p[e] = __fmaf_rn(-wd, p[e], __fmaf_rn(-a.lr, u, p[e]));
-                if (e < cnt) nan_sum = __fmaf_rn(v[e], 0.0f, __fmaf_rn(p[e], 0.0f, nan_sum));
-                if (coded) v[e] = root;
-            }
-            if (d.p_type == SF_TYPE_F32) store8_f32(static_cast<float *>(d.p) + at, p, cnt);
-            else store8_bf16(static_cast<uint16_t *>(d.p) + at, p, cnt);
-            if (d.live) store8_bf16(d.live + at, p, cnt);
-            if (coded) {
-                encode8<false>(m, d.m, at, cnt, d.m_scale + blk, lane);
-                encode8<true>(v, d.v, at, cnt, d.v_scale + blk, lane);
-            } else {
-                store8_f32(static_cast<float *>(d.m) + at, m, cnt);
-                store8_f32(static_cast<float *>(d.v) + at, v, cnt);
-            }
+            for (int e = 0; e < 8; ++e) nan_sum = __fmaf_rn(p[e], 0.0f, nan_sum);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < cnt) nan_sum = __fmaf_rn(p[e], 0.0f, nan_sum);
+        }
+        if (d.p_type == SF_TYPE_F32) store8_f32(static_cast<float *>(d.p) + first, p, cnt);
+        else store8_bf16(static_cast<uint16_t *>(d.p) + first, p, cnt);
+        if (d.live) store8_bf16(d.live + first, p, cnt);
+        if (CODED) {                                 // a scale is the largest moment's: not finite where one of them is not
+            nan_sum = __fmaf_rn(encode8<false>(m, d.m, first, cnt, d.m_scale + blk, lane), 0.0f, nan_sum);
+            nan_sum = __fmaf_rn(encode8<true>(v, d.v, first, cnt, d.v_scale + blk, lane), 0.0f, nan_sum);
+        } else {
+            store8_f32(static_cast<float *>(d.m) + first, m, cnt);
+            store8_f32(static_cast<float *>(d.v) + first, v, cnt);
+            if (at.there()) cur.load(b.d[at.which], at.blk, lane);
         }
     }
     if (nan_sum != 0.0f) set_status(status, SF_STATUS_NONFINITE);
@@ -277,8 +378,9 @@ constexpr size_t kNormHeader = 16;
 
 // Sum of squares: fp32 over a lane's eight elements, fp64 from there. Every CTA leaves its sum in its own
 // place; the last one of the call adds them in a fixed order.
+template <int N>
 __global__ void __launch_bounds__(kThreads)
-grad_norm_kernel(const __grid_constant__ DenseBatch b, int32_t *done, double *sums, int at0, int total_ctas,
+grad_norm_kernel(const __grid_constant__ DenseBatch<N> b, int32_t *done, double *sums, int at0, int total_ctas,
                  float inv_scale, float max_norm, float *out, uint32_t *status)
 {
     __shared__ double part[kWarps];
@@ -286,18 +388,26 @@ grad_norm_kernel(const __grid_constant__ DenseBatch b, int32_t *done, double *su
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     double sum = 0.0;
     for (int unit = blockIdx.x; unit < b.units; unit += gridDim.x) {
-        const DenseDesc &d = b.d[find_tensor(b, unit)];
-        const int64_t first = (int64_t)(unit - d.unit_begin) * b.per * kWarps;
-#pragma unroll 4
-        for (int k = 0; k < b.per; ++k) {
-            const int64_t at = (first + (int64_t)k * kWarps + warp) * kBlock + lane * kLaneElems;
-            const int cnt = (int)max((int64_t)0, min((int64_t)8, d.n - at));
-            float g[8];
-            load8(g, d.g, d.g_type, at, cnt);
-            float s = 0.0f;
+        const int which = find_tensor(b, unit);
+        const DenseDesc &d = b.d[which];
+        const int64_t first = ((int64_t)(unit - b.unit_begin[which]) * b.per * kWarps + warp) * kBlock + lane * kLaneElems;
+        constexpr int64_t kStride = (int64_t)kWarps * kBlock;
+        for (int k = 0; k < b.per; k += 4) {        // four blocks' loads at once
+            Raw8 r[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s = __fmaf_rn(g[e], g[e], s);
-            sum += (double)s;
+            for (int q = 0; q < 4; ++q) {
+                const int64_t at = first + (k + q) * kStride;
+                const int cnt = k + q < b.per ? (int)max((int64_t)0, min((int64_t)8, d.n - at)) : 0;
+                r[q] = load_raw(d.g, d.g_type, at, cnt);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float g[8], s = 0.0f;
+                to_float(g, r[q], d.g_type);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s = __fmaf_rn(g[e], g[e], s);
+                sum += (double)s;
+            }
         }
     }
 #pragma unroll
@@ -369,15 +479,18 @@ int unit_blocks(const sf_dense *t, int n, int sms)
     return each >= 8 ? 8 : each >= 4 ? 4 : each >= 2 ? 2 : 1;
 }
 
-// The next launch's tensors, from *at on. Returns the units, or -1 when they pass 2^31.
-int64_t fill(DenseBatch &b, const sf_dense *t, int n, int *at, int per)
+// The next launch's tensors, from *at on: those with moments of the given type, or all (-1). Returns the units, or -1
+// when they pass 2^30.
+template <int N>
+int64_t fill(DenseBatch<N> &b, const sf_dense *t, int n, int *at, int per, int state)
 {
     b.n = 0;
     b.per = per;
     int64_t units = 0;
-    for (; *at < n && b.n < kMaxTensors; ++*at) {
+    for (; *at < n && b.n < N; ++*at) {
         const sf_dense &a = t[*at];
-        if (a.n == 0) continue;
+        if (a.n == 0 || (state >= 0 && a.state_type != state)) continue;
+        b.unit_begin[b.n] = (int32_t)units;
         DenseDesc &d = b.d[b.n++];
         d.n = a.n;
         d.p = a.p;
@@ -392,19 +505,84 @@ int64_t fill(DenseBatch &b, const sf_dense *t, int n, int *at, int per)
         d.g_type = (uint8_t)a.g_type;
         d.state_type = (uint8_t)a.state_type;
         d.pad = 0;
-        d.unit_begin = (int32_t)units;
         units += (a.n + (int64_t)per * kWarps * kBlock - 1) / ((int64_t)per * kWarps * kBlock);
-        if (units > INT32_MAX / 2) return -1;
+        if (units > 1 << 30) return -1;
     }
     b.units = (int32_t)units;
     return units;
 }
 
-int count_launches(const sf_dense *t, int n)
+// Tensors with elements, with moments of the given type or of any (-1).
+int full_tensors(const sf_dense *t, int n, int state)
 {
     int full = 0;
-    for (int i = 0; i < n; ++i) full += t[i].n > 0;
-    return (full + kMaxTensors - 1) / kMaxTensors;
+    for (int i = 0; i < n; ++i) full += t[i].n > 0 && (state < 0 || t[i].state_type == state);
+    return full;
+}
+
+int count_launches(const sf_dense *t, int n) { return (full_tensors(t, n, -1) + kMaxTensors - 1) / kMaxTensors; }
+
+struct NormArgs {
+    float inv_scale, max_norm;
+    float *out;
+    void *ws;
+    uint32_t *status;
+    cudaStream_t stream;
+};
+
+template <int N>
+int launch_norm(const sf_dense *t, int n, int sms, const NormArgs &a)
+{
+    const int per = unit_blocks(t, n, sms);
+    const int64_t cap = (int64_t)sms * kMaxGridPerSm;
+    DenseBatch<N> b;
+    // the CTAs of all launches, so that the last one of them knows itself
+    int64_t total = 0;
+    for (int at = 0, first = 1; first || at < n; first = 0) {
+        const int64_t units = fill(b, t, n, &at, per, -1);
+        if (units < 0) return SF_ERR_UNSUPPORTED;
+        if (units > 0 || first) total += units < cap ? (units > 0 ? units : 1) : cap;
+    }
+    int32_t *done = static_cast<int32_t *>(a.ws);
+    double *sums = reinterpret_cast<double *>(static_cast<char *>(a.ws) + kNormHeader);
+    int64_t placed = 0;
+    for (int at = 0, first = 1; first || at < n; first = 0) {
+        const int64_t units = fill(b, t, n, &at, per, -1);
+        if (units == 0 && !first) continue;
+        const int64_t grid = units < cap ? (units > 0 ? units : 1) : cap;
+        grad_norm_kernel<N><<<(int)grid, kThreads, 0, a.stream>>>(b, done, sums, (int)placed, (int)total, a.inv_scale,
+                                                                 a.max_norm, a.out, a.status);
+        if (launch_status() != SF_OK) return SF_ERR_CUDA;
+        placed += grid;
+    }
+    return SF_OK;
+}
+
+// The tensors with moments of one type; `last`: no launch of the call follows.
+template <int N, bool CODED>
+int launch_step(const sf_dense *t, int n, int sms, int per, bool last, StepArgs a, uint32_t *status, cudaStream_t stream)
+{
+    const int state = CODED ? SF_TYPE_E4M3 : SF_TYPE_F32;
+    const int launches = (full_tensors(t, n, state) + N - 1) / N;
+    const int64_t cap = (int64_t)sms * kMaxGridPerSm;
+    DenseBatch<N> b;
+    for (int at = 0, li = 0; li < launches; ++li) {
+        const int64_t units = fill(b, t, n, &at, per, state);
+        if (units < 0) return SF_ERR_UNSUPPORTED;
+        a.last = last && li == launches - 1;
+        adamw_kernel<N, CODED><<<(int)(units < cap ? units : cap), kThreads, 0, stream>>>(b, a, status);
+        if (launch_status() != SF_OK) return SF_ERR_CUDA;
+    }
+    return SF_OK;
+}
+
+template <bool CODED>
+int launch_steps(const sf_dense *t, int n, int sms, int per, bool last, const StepArgs &a, uint32_t *status, cudaStream_t stream)
+{
+    const int full = full_tensors(t, n, CODED ? SF_TYPE_E4M3 : SF_TYPE_F32);
+    return full <= kFew ? launch_step<kFew, CODED>(t, n, sms, per, last, a, status, stream)
+           : full <= kSome ? launch_step<kSome, CODED>(t, n, sms, per, last, a, status, stream)
+                           : launch_step<kMaxTensors, CODED>(t, n, sms, per, last, a, status, stream);
 }
 
 }  // namespace
@@ -431,29 +609,10 @@ extern "C" int sf_grad_norm(const sf_dense *t, int n, float inv_scale, float max
     const int sms = sm_count();
     if (sms <= 0) return SF_ERR_NO_DEVICE;
     if (sms > 256) return SF_ERR_UNSUPPORTED;
-    const int per = unit_blocks(t, n, sms);
-    const int64_t cap = (int64_t)sms * kMaxGridPerSm;
-    DenseBatch b;
-    // the CTAs of all launches, so that the last one of them knows itself
-    int64_t total = 0;
-    for (int at = 0, first = 1; first || at < n; first = 0) {
-        const int64_t units = fill(b, t, n, &at, per);
-        if (units < 0) return SF_ERR_UNSUPPORTED;
-        if (units > 0 || first) total += units < cap ? (units > 0 ? units : 1) : cap;
-    }
-    int32_t *done = static_cast<int32_t *>(ws);
-    double *sums = reinterpret_cast<double *>(static_cast<char *>(ws) + kNormHeader);
-    int64_t placed = 0;
-    for (int at = 0, first = 1; first || at < n; first = 0) {
-        const int64_t units = fill(b, t, n, &at, per);
-        if (units == 0 && !first) continue;
-        const int64_t grid = units < cap ? (units > 0 ? units : 1) : cap;
-        grad_norm_kernel<<<(int)grid, kThreads, 0, as_stream(stream)>>>(b, done, sums, (int)placed, (int)total,
-                                                                       inv_scale, max_norm, out, dev_status);
-        if (launch_status() != SF_OK) return SF_ERR_CUDA;
-        placed += grid;
-    }
-    return SF_OK;
+    const NormArgs a = {inv_scale, max_norm, out, ws, dev_status, as_stream(stream)};
+    const int full = full_tensors(t, n, -1);
+    return full <= kFew ? launch_norm<kFew>(t, n, sms, a) : full <= kSome ? launch_norm<kSome>(t, n, sms, a)
+                        : launch_norm<kMaxTensors>(t, n, sms, a);
 }
 
 extern "C" int sf_adamw_step(const sf_dense *t, int n, const sf_adam *hp, int32_t *step, const float *factor,
@@ -479,20 +638,15 @@ extern "C" int sf_adamw_step(const sf_dense *t, int n, const sf_adam *hp, int32_
     a.t_max = hp->t_max;
     a.step = step;
     a.factor = factor;
-    const int launches = count_launches(t, n);
-    if (launches == 0) {
+    const int coded = full_tensors(t, n, SF_TYPE_E4M3), full = full_tensors(t, n, -1);
+    if (full == 0) {
         count_step_kernel<<<1, 1, 0, as_stream(stream)>>>(step, factor, dev_status);
         return launch_status();
     }
     const int per = unit_blocks(t, n, sms);
-    DenseBatch b;
-    for (int at = 0, li = 0; li < launches; ++li) {
-        const int64_t units = fill(b, t, n, &at, per);
-        if (units < 0) return SF_ERR_UNSUPPORTED;
-        a.last = li == launches - 1;
-        const int64_t cap = (int64_t)sms * kMaxGridPerSm;
-        adamw_kernel<<<(int)(units < cap ? units : cap), kThreads, 0, as_stream(stream)>>>(b, a, dev_status);
-        if (launch_status() != SF_OK) return SF_ERR_CUDA;
+    if (full > coded) {
+        rc = launch_steps<false>(t, n, sms, per, coded == 0, a, dev_status, as_stream(stream));
+        if (rc != SF_OK) return rc;
     }
-    return SF_OK;
+    return coded ? launch_steps<true>(t, n, sms, per, true, a, dev_status, as_stream(stream)) : SF_OK;
 }
