@@ -51,8 +51,43 @@ struct DenseBatch {
 static_assert(sizeof(DenseBatch<kMaxTensors>) <= 32000, "kernel parameter space");
 constexpr int kFew = 16, kSome = 96;
 
+// Two fp32 values in one 64-bit register pair, and the operations of sm_100 that take both at once, each rounded as
+// its scalar form. The step with 8-bit moments is held up by the instructions it issues, not by memory alone.
+typedef uint64_t pair_t;
+__device__ __forceinline__ pair_t pair_of(float a, float b)
+{
+    pair_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 halves(pair_t p)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b)
+{
+    pair_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ pair_t add2(pair_t a, pair_t b)
+{
+    pair_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c)
+{
+    pair_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 struct StepArgs {
-    float beta1, beta2, omb1, omb2, eps, lr, wd, clip;
+    pair_t beta1, beta2, omb1, omb2, eps, minus_lr;       // each value twice
+    float lr, wd, clip;
     const float *bc1, *bc2;
     int32_t t_max, last;                      // last: this launch ends the call
     int32_t *step;
@@ -70,19 +105,46 @@ __device__ __forceinline__ int find_tensor(const DenseBatch<N> &b, int unit)
     return lo;
 }
 
-// A lane's eight consecutive elements as they lie in memory: 16 bytes of 16-bit values, 32 of fp32. The first `cnt` are
-// loaded, the rest are zero.
+// Square roots by one step of Heron's iteration from the hardware's approximate reciprocal root y: with r = x y, the
+// residual r r - x is exact in one fused operation, and r - (r r - x) y / 2 is the root to the last place (tests hold it
+// to the correctly rounded one). The library's root, with its paths for numbers outside the normal ones, took a third of
+// the step's instructions. Zero gives zero. The residual is a multiple of 2^-149, so it is off by up to 2^-150 and the
+// root by up to 2^-150 y / 2, which is 2^-151 / x of it: nothing down to 2^-100, a quarter of a step at 2^-126.
+__device__ __forceinline__ pair_t root2_of(pair_t x)
+{
+    const float2 v = halves(x);
+    float ya, yb;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(ya) : "f"(fmaxf(v.x, 0x1p-149f)));
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(yb) : "f"(fmaxf(v.y, 0x1p-149f)));
+    const pair_t y = pair_of(ya, yb), r = mul2(x, y);
+    const pair_t off = fma2(r, r, mul2(x, pair_of(-1.0f, -1.0f)));
+    return fma2(off, mul2(y, pair_of(-0.5f, -0.5f)), r);
+}
+
+// a / b within 2 units in the last place for the sizes that occur here (b normal, below 2^126).
+__device__ __forceinline__ pair_t ratio2(pair_t a, pair_t b)
+{
+    const float2 v = halves(b);
+    float ya, yb;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ya) : "f"(v.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(yb) : "f"(v.y));
+    return mul2(a, pair_of(ya, yb));
+}
+
+// A lane's eight consecutive elements as they lie in memory: 16 bytes of 16-bit values, 32 of fp32. With FULL all eight
+// are there; without, the first `cnt`, and the rest are zero.
 struct Raw8 {
     uint4 a, b;
 };
 
+template <bool FULL>
 __device__ __forceinline__ Raw8 load_raw(const void *base, int type, int64_t at, int cnt)
 {
     Raw8 r;
     r.a = r.b = make_uint4(0u, 0u, 0u, 0u);
     if (type == SF_TYPE_F32) {
         const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + at);
-        if (cnt == 8) {
+        if (FULL || cnt == 8) {
             r.a = __ldcs(src);
             r.b = __ldcs(src + 1);
         } else if (cnt > 0) {
@@ -92,58 +154,62 @@ __device__ __forceinline__ Raw8 load_raw(const void *base, int type, int64_t at,
         }
     } else {
         const uint16_t *src = static_cast<const uint16_t *>(base) + at;
-        if (cnt == 8) {
+        if (FULL || cnt == 8) {
             r.a = __ldcs(reinterpret_cast<const uint4 *>(src));
         } else if (cnt > 0) {
-            auto pair = [&](int e) { return (e < cnt ? (uint32_t)src[e] : 0u) | (e + 1 < cnt ? (uint32_t)src[e + 1] << 16 : 0u); };
-            r.a = make_uint4(pair(0), pair(2), pair(4), pair(6));
+            auto two = [&](int e) { return (e < cnt ? (uint32_t)src[e] : 0u) | (e + 1 < cnt ? (uint32_t)src[e + 1] << 16 : 0u); };
+            r.a = make_uint4(two(0), two(2), two(4), two(6));
         }
     }
     return r;
 }
 
-__device__ __forceinline__ void to_float(float (&x)[8], const Raw8 &r, int type)
+__device__ __forceinline__ void to_pairs(pair_t (&x)[4], const Raw8 &r, int type)
 {
-    if (type == SF_TYPE_F32) {
-        x[0] = __uint_as_float(r.a.x); x[1] = __uint_as_float(r.a.y); x[2] = __uint_as_float(r.a.z); x[3] = __uint_as_float(r.a.w);
-        x[4] = __uint_as_float(r.b.x); x[5] = __uint_as_float(r.b.y); x[6] = __uint_as_float(r.b.z); x[7] = __uint_as_float(r.b.w);
-        return;
-    }
     const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+    if (type == SF_TYPE_F32) {
+        x[0] = pair_of(__uint_as_float(r.a.x), __uint_as_float(r.a.y));
+        x[1] = pair_of(__uint_as_float(r.a.z), __uint_as_float(r.a.w));
+        x[2] = pair_of(__uint_as_float(r.b.x), __uint_as_float(r.b.y));
+        x[3] = pair_of(__uint_as_float(r.b.z), __uint_as_float(r.b.w));
+    } else if (type == SF_TYPE_BF16) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        if (type == SF_TYPE_BF16) {
-            x[2 * e] = __uint_as_float(w[e] << 16);
-            x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-        } else {
+        for (int e = 0; e < 4; ++e) x[e] = pair_of(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
             const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
-            x[2 * e] = h.x;
-            x[2 * e + 1] = h.y;
+            x[e] = pair_of(h.x, h.y);
         }
     }
 }
 
-__device__ __forceinline__ void store8_f32(float *dst, const float (&x)[8], int cnt)
+template <bool FULL>
+__device__ __forceinline__ void store8_f32(float *dst, const pair_t (&x)[4], int cnt)
 {
-    if (cnt == 8) {
-        __stcs(reinterpret_cast<float4 *>(dst), make_float4(x[0], x[1], x[2], x[3]));
-        __stcs(reinterpret_cast<float4 *>(dst) + 1, make_float4(x[4], x[5], x[6], x[7]));
+    const float2 a = halves(x[0]), b = halves(x[1]), c = halves(x[2]), d = halves(x[3]);
+    if (FULL || cnt == 8) {
+        __stcs(reinterpret_cast<float4 *>(dst), make_float4(a.x, a.y, b.x, b.y));
+        __stcs(reinterpret_cast<float4 *>(dst) + 1, make_float4(c.x, c.y, d.x, d.y));
     } else {
+        const float v[8] = {a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (e < cnt) dst[e] = x[e];
+            if (e < cnt) dst[e] = v[e];
     }
 }
 
-__device__ __forceinline__ void store8_bf16(uint16_t *dst, const float (&x)[8], int cnt)
+template <bool FULL>
+__device__ __forceinline__ void store8_bf16(uint16_t *dst, const pair_t (&x)[4], int cnt)
 {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+        const float2 v = halves(x[e]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
         w[e] = *reinterpret_cast<const uint32_t *>(&h);
     }
-    if (cnt == 8) {
+    if (FULL || cnt == 8) {
         __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(w[0], w[1], w[2], w[3]));
     } else {
 #pragma unroll
@@ -153,10 +219,11 @@ __device__ __forceinline__ void store8_bf16(uint16_t *dst, const float (&x)[8], 
 }
 
 // Eight e4m3 codes (zeros behind cnt) as two words.
+template <bool FULL>
 __device__ __forceinline__ uint2 load8_codes(const void *base, int64_t at, int cnt)
 {
     const uint8_t *src = static_cast<const uint8_t *>(base) + at;
-    if (cnt == 8) return __ldcs(reinterpret_cast<const uint2 *>(src));
+    if (FULL || cnt == 8) return __ldcs(reinterpret_cast<const uint2 *>(src));
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -164,42 +231,48 @@ __device__ __forceinline__ uint2 load8_codes(const void *base, int64_t at, int c
     return make_uint2(w[0], w[1]);
 }
 
-__device__ __forceinline__ void decode8(float (&x)[8], uint2 codes, float scale)
+__device__ __forceinline__ void decode8(pair_t (&x)[4], uint2 codes, float scale)
 {
+    const pair_t s = pair_of(scale, scale);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const uint32_t w = e < 2 ? codes.x : codes.y;
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * (e & 1))), __NV_E4M3);
         const float2 f = __half22float2(__half2(h));
-        x[2 * e] = __fmul_rn(f.x, scale);
-        x[2 * e + 1] = __fmul_rn(f.y, scale);
+        x[e] = mul2(pair_of(f.x, f.y), s);
     }
 }
 
 // Codes and scale of a block's values (this lane's eight); returns the scale. POSITIVE: no value is negative, and a value
 // above zero keeps a code above zero.
-template <bool POSITIVE>
-__device__ __forceinline__ float encode8(const float (&x)[8], void *base, int64_t at, int cnt, float *scale, int lane)
+template <bool FULL, bool POSITIVE>
+__device__ __forceinline__ float encode8(const pair_t (&x)[4], void *base, int64_t at, int cnt, float *scale, int lane)
 {
     uint32_t big = 0;                                // magnitudes order as their bits; a NaN is the largest
 #pragma unroll
-    for (int e = 0; e < 8; ++e) big = max(big, POSITIVE ? __float_as_uint(x[e]) : __float_as_uint(x[e]) & 0x7FFFFFFFu);
+    for (int e = 0; e < 4; ++e) {
+        const float2 v = halves(x[e]);
+        const uint32_t a = __float_as_uint(v.x), b = __float_as_uint(v.y);
+        big = max(big, POSITIVE ? max(a, b) : max(a & 0x7FFFFFFFu, b & 0x7FFFFFFFu));
+    }
     big = __reduce_max_sync(0xffffffffu, big);
     float sc = __fmul_rn(__uint_as_float(big), 1.0f / 448.0f);
     if (sc < kScaleFloor) sc = kScaleFloor;          // a NaN stays
     const float inv = __frcp_rn(sc);
+    const pair_t inv2 = pair_of(inv, inv);
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        float a = __fmul_rn(x[2 * e], inv), b = __fmul_rn(x[2 * e + 1], inv);
+        float2 v = halves(mul2(x[e], inv2));
         if (POSITIVE) {
-            if (x[2 * e] > 0.0f) a = fmaxf(a, kSmallestCode);
-            if (x[2 * e + 1] > 0.0f) b = fmaxf(b, kSmallestCode);
+            const float2 was = halves(x[e]);
+            if (was.x > 0.0f) v.x = fmaxf(v.x, kSmallestCode);
+            if (was.y > 0.0f) v.y = fmaxf(v.y, kSmallestCode);
         }
-        w[e >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) << (16 * (e & 1));
+        w[e >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3) << (16 * (e & 1));
     }
     uint8_t *dst = static_cast<uint8_t *>(base) + at;
-    if (cnt == 8) {
+    if (FULL || cnt == 8) {
         __stcs(reinterpret_cast<uint2 *>(dst), make_uint2(w[0], w[1]));
     } else {
 #pragma unroll
@@ -246,17 +319,22 @@ struct Block {
     __device__ __forceinline__ void load(const DenseDesc &d, int64_t blk, int lane)
     {
         const int64_t at = blk * kBlock + lane * kLaneElems;
-        const int cnt = (int)max((int64_t)0, min((int64_t)8, d.n - at));
-        p = load_raw(d.p, d.p_type, at, cnt);
-        g = load_raw(d.g, d.g_type, at, cnt);
+        if ((blk + 1) * kBlock <= d.n) load_from<true>(d, blk, at, 8);
+        else load_from<false>(d, blk, at, (int)max((int64_t)0, min((int64_t)8, d.n - at)));
+    }
+    template <bool FULL>
+    __device__ __forceinline__ void load_from(const DenseDesc &d, int64_t blk, int64_t at, int cnt)
+    {
+        p = load_raw<FULL>(d.p, d.p_type, at, cnt);
+        g = load_raw<FULL>(d.g, d.g_type, at, cnt);
         if (CODED) {
-            cm = load8_codes(d.m, at, cnt);
-            cv = load8_codes(d.v, at, cnt);
+            cm = load8_codes<FULL>(d.m, at, cnt);
+            cv = load8_codes<FULL>(d.v, at, cnt);
             sm = d.m_scale[blk];
             sv = d.v_scale[blk];
         } else {
-            m = load_raw(d.m, SF_TYPE_F32, at, cnt);
-            v = load_raw(d.v, SF_TYPE_F32, at, cnt);
+            m = load_raw<FULL>(d.m, SF_TYPE_F32, at, cnt);
+            v = load_raw<FULL>(d.v, SF_TYPE_F32, at, cnt);
         }
     }
 };
@@ -267,24 +345,90 @@ __device__ __forceinline__ void prefetch_block(const DenseDesc &d, int64_t blk, 
 {
     const int p_size = d.p_type == SF_TYPE_F32 ? 4 : 2, g_size = d.g_type == SF_TYPE_F32 ? 4 : 2;
     const char *base = static_cast<const char *>(lane < 8 ? d.p : lane < 16 ? d.g : lane < 24 ? d.m : d.v);
-    const int size = lane < 8 ? p_size : lane < 16 ? g_size : 1, line = lane & 7;
+    const int s_size = d.state_type == SF_TYPE_F32 ? 4 : 1;
+    const int size = lane < 8 ? p_size : lane < 16 ? g_size : s_size, line = lane & 7;
     const int64_t off = blk * kBlock * size + line * 128;
     if (line < 2 * size && off < d.n * size) prefetch_l2(base + off);
 }
 
-// With fp32 moments a block's loads (3.5 KB a warp) are issued behind the stores of the block before, in registers: 900 us
-// for a 7B-shaped layer, 6.3 TB/s. With 8-bit moments they are 2 KB and the arithmetic takes about as long as the memory
-// (a correctly rounded quotient in place of the approximate one costs 6%), so a block is loaded where it is used, the
-// next one is asked for in L2 before that, and four CTAs to an SM hide one another's waits.
+struct StepNow {
+    pair_t bc1, root_bc2, factor;
+};
+
+// One block's step on what was loaded: this lane's eight elements. FULL: the block has all its 256.
+template <bool CODED, bool FULL>
+__device__ __forceinline__ void step_block(const Block<CODED> &in, const DenseDesc &d, int64_t blk, const StepArgs &a, const StepNow &now,
+                                           int lane, pair_t &nan_sum)
+{
+    const int64_t at = blk * kBlock + lane * kLaneElems;
+    const int cnt = FULL ? 8 : (int)max((int64_t)0, min((int64_t)8, d.n - at));
+    pair_t p[4], g[4], m[4], v[4];
+    to_pairs(p, in.p, d.p_type);
+    to_pairs(g, in.g, d.g_type);
+    if (CODED) {
+        decode8(m, in.cm, in.sm);
+        decode8(v, in.cv, in.sv);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], v[e]);
+    } else {
+        to_pairs(m, in.m, SF_TYPE_F32);
+        to_pairs(v, in.v, SF_TYPE_F32);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) g[e] = mul2(g[e], now.factor);
+    if (a.clip > 0.0f) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 x = halves(g[e]);
+            g[e] = pair_of(fminf(fmaxf(x.x, -a.clip), a.clip), fminf(fmaxf(x.y, -a.clip), a.clip));
+        }
+    }
+    const float wd = __fmul_rn(d.decay, __fmul_rn(a.lr, a.wd));
+    const pair_t minus_wd = pair_of(-wd, -wd), zero = pair_of(0.0f, 0.0f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        m[e] = add2(mul2(m[e], a.beta1), mul2(g[e], a.omb1));
+        v[e] = add2(mul2(v[e], a.beta2), mul2(mul2(g[e], g[e]), a.omb2));
+        const pair_t root = root2_of(v[e]);
+        const pair_t u = ratio2(mul2(m[e], now.bc1), fma2(root, now.root_bc2, a.eps));
+        p[e] = fma2(minus_wd, p[e], fma2(a.minus_lr, u, p[e]));
+        if (FULL) {                                  // x * 0 is 0 for every finite x, and NaN otherwise
+            nan_sum = fma2(p[e], zero, nan_sum);
+            if (!CODED) nan_sum = fma2(v[e], zero, nan_sum);
+        } else {                                     // elements behind the end are not looked at
+            const float2 x = halves(p[e]), y = halves(v[e]);
+            nan_sum = fma2(pair_of(2 * e < cnt ? x.x : 0.0f, 2 * e + 1 < cnt ? x.y : 0.0f), zero, nan_sum);
+            if (!CODED) nan_sum = fma2(pair_of(2 * e < cnt ? y.x : 0.0f, 2 * e + 1 < cnt ? y.y : 0.0f), zero, nan_sum);
+        }
+        if (CODED) v[e] = root;
+    }
+    if (d.p_type == SF_TYPE_F32) store8_f32<FULL>(static_cast<float *>(d.p) + at, p, cnt);
+    else store8_bf16<FULL>(static_cast<uint16_t *>(d.p) + at, p, cnt);
+    if (d.live) store8_bf16<FULL>(d.live + at, p, cnt);
+    if (CODED) {                                     // a scale is the largest moment's: not finite where one of them is not
+        const float sm = encode8<FULL, false>(m, d.m, at, cnt, d.m_scale + blk, lane);
+        const float sv = encode8<FULL, true>(v, d.v, at, cnt, d.v_scale + blk, lane);
+        nan_sum = fma2(pair_of(sm, sv), zero, nan_sum);
+    } else {
+        store8_f32<FULL>(static_cast<float *>(d.m) + at, m, cnt);
+        store8_f32<FULL>(static_cast<float *>(d.v) + at, v, cnt);
+    }
+}
+
+// With fp32 moments a block's loads (3.5 KB a warp) are issued behind the stores of the block before. With 8-bit moments
+// they are 2 KB and the instructions take most of the memory's time, so four CTAs to an SM hide one another's waits: a
+// block is loaded where it is used, and its lines are asked for in L2 one block ahead.
 template <int N, bool CODED>
 __global__ void __launch_bounds__(kThreads, CODED ? 4 : 3)
-adamw_kernel(const __grid_constant__ DenseBatch<N> b, const StepArgs a, uint32_t *status)
+adamw_kernel(const __grid_constant__ DenseBatch<N> b, const __grid_constant__ StepArgs a, uint32_t *status)
 {
     const int lane = threadIdx.x & 31;
     Cursor<N> at(b);
-    Block<CODED> cur;
-    if (!CODED && at.there()) cur.load(b.d[at.which], at.blk, lane);     // before the step's own words: two trips to memory
-    if (CODED && at.there()) prefetch_block(b.d[at.which], at.blk, lane);
+    Block<CODED> in;
+    if (at.there()) {                                // before the step's own words, which take two trips to memory
+        if (CODED) prefetch_block(b.d[at.which], at.blk, lane);
+        else in.load(b.d[at.which], at.blk, lane);
+    }
     const int t = a.step[0] + 1;
     const float f = a.factor ? a.factor[1] : 1.0f;
     if (!(f != 0.0f) || f != f) {                    // the gradient was not finite: leave everything
@@ -292,66 +436,22 @@ adamw_kernel(const __grid_constant__ DenseBatch<N> b, const StepArgs a, uint32_t
         return;
     }
     const int ti = t < 0 ? 0 : t < a.t_max ? t : a.t_max;
-    const float bc1 = a.bc1[ti], root2 = __fsqrt_rn(a.bc2[ti]);
-    float nan_sum = 0.0f;                            // stays 0 while everything is finite
+    const float bc1 = a.bc1[ti], root = __fsqrt_rn(a.bc2[ti]);
+    const StepNow now = {pair_of(bc1, bc1), pair_of(root, root), pair_of(f, f)};
+    pair_t nan_sum = pair_of(0.0f, 0.0f);            // stays 0 while everything is finite
 
     while (at.there()) {
         const DenseDesc &d = b.d[at.which];
-        const int64_t blk = at.blk, first = blk * kBlock + lane * kLaneElems;
-        const int cnt = (int)max((int64_t)0, min((int64_t)8, d.n - first));
-        if (CODED) cur.load(d, blk, lane);
+        const int64_t blk = at.blk;
+        if (CODED) in.load(d, blk, lane);
         at.next();
         if (CODED && at.there()) prefetch_block(b.d[at.which], at.blk, lane);
-        float p[8], g[8], m[8], v[8];
-        to_float(p, cur.p, d.p_type);
-        to_float(g, cur.g, d.g_type);
-        if (CODED) {
-            decode8(m, cur.cm, cur.sm);
-            decode8(v, cur.cv, cur.sv);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], v[e]);
-        } else {
-            to_float(m, cur.m, SF_TYPE_F32);
-            to_float(v, cur.v, SF_TYPE_F32);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], f);
-        if (a.clip > 0.0f) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = fminf(fmaxf(g[e], -a.clip), a.clip);
-        }
-        const float wd = __fmul_rn(d.decay, __fmul_rn(a.lr, a.wd));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            m[e] = __fadd_rn(__fmul_rn(m[e], a.beta1), __fmul_rn(g[e], a.omb1));
-            v[e] = __fadd_rn(__fmul_rn(v[e], a.beta2), __fmul_rn(__fmul_rn(g[e], g[e]), a.omb2));
-            const float root = __fsqrt_rn(v[e]);
-            const float u = __fdividef(__fmul_rn(m[e], bc1), __fmaf_rn(root, root2, a.eps));
-            p[e] = __fmaf_rn(-wd, p[e], __fmaf_rn(-a.lr, u, p[e]));
-            if (!CODED && e < cnt) nan_sum = __fmaf_rn(v[e], 0.0f, nan_sum);
-            if (CODED) v[e] = root;
-        }
-        if (cnt == 8) {                              // elements behind the end are not looked at
-#pragma unroll
-            for (int e = 0; e < 8; ++e) nan_sum = __fmaf_rn(p[e], 0.0f, nan_sum);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < cnt) nan_sum = __fmaf_rn(p[e], 0.0f, nan_sum);
-        }
-        if (d.p_type == SF_TYPE_F32) store8_f32(static_cast<float *>(d.p) + first, p, cnt);
-        else store8_bf16(static_cast<uint16_t *>(d.p) + first, p, cnt);
-        if (d.live) store8_bf16(d.live + first, p, cnt);
-        if (CODED) {                                 // a scale is the largest moment's: not finite where one of them is not
-            nan_sum = __fmaf_rn(encode8<false>(m, d.m, first, cnt, d.m_scale + blk, lane), 0.0f, nan_sum);
-            nan_sum = __fmaf_rn(encode8<true>(v, d.v, first, cnt, d.v_scale + blk, lane), 0.0f, nan_sum);
-        } else {
-            store8_f32(static_cast<float *>(d.m) + first, m, cnt);
-            store8_f32(static_cast<float *>(d.v) + first, v, cnt);
-            if (at.there()) cur.load(b.d[at.which], at.blk, lane);
-        }
+        if ((blk + 1) * kBlock <= d.n) step_block<CODED, true>(in, d, blk, a, now, lane, nan_sum);
+        else step_block<CODED, false>(in, d, blk, a, now, lane, nan_sum);
+        if (!CODED && at.there()) in.load(b.d[at.which], at.blk, lane);
     }
-    if (nan_sum != 0.0f) set_status(status, SF_STATUS_NONFINITE);
+    const float2 bad = halves(nan_sum);
+    if (bad.x != 0.0f || bad.y != 0.0f) set_status(status, SF_STATUS_NONFINITE);
     // The last CTA to finish counts the step: by then every CTA has read the old count.
     if (a.last) {
         __syncthreads();
@@ -398,15 +498,16 @@ grad_norm_kernel(const __grid_constant__ DenseBatch<N> b, int32_t *done, double 
             for (int q = 0; q < 4; ++q) {
                 const int64_t at = first + (k + q) * kStride;
                 const int cnt = k + q < b.per ? (int)max((int64_t)0, min((int64_t)8, d.n - at)) : 0;
-                r[q] = load_raw(d.g, d.g_type, at, cnt);
+                r[q] = load_raw<false>(d.g, d.g_type, at, cnt);
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                float g[8], s = 0.0f;
-                to_float(g, r[q], d.g_type);
+                pair_t g[4], s = pair_of(0.0f, 0.0f);
+                to_pairs(g, r[q], d.g_type);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s = __fmaf_rn(g[e], g[e], s);
-                sum += (double)s;
+                for (int e = 0; e < 4; ++e) s = fma2(g[e], g[e], s);
+                const float2 both = halves(s);
+                sum += (double)__fadd_rn(both.x, both.y);
             }
         }
     }
@@ -625,11 +726,17 @@ extern "C" int sf_adamw_step(const sf_dense *t, int n, const sf_adam *hp, int32_
     const int sms = sm_count();
     if (sms <= 0) return SF_ERR_NO_DEVICE;
     StepArgs a;
-    a.beta1 = hp->beta1;
-    a.beta2 = hp->beta2;
-    a.omb1 = hp->one_minus_b1;
-    a.omb2 = hp->one_minus_b2;
-    a.eps = hp->eps;
+    auto twice = [](float x) {
+        uint32_t w;
+        memcpy(&w, &x, 4);
+        return (pair_t)w << 32 | w;
+    };
+    a.beta1 = twice(hp->beta1);
+    a.beta2 = twice(hp->beta2);
+    a.omb1 = twice(hp->one_minus_b1);
+    a.omb2 = twice(hp->one_minus_b2);
+    a.eps = twice(hp->eps);
+    a.minus_lr = twice(-hp->lr);
     a.lr = hp->lr;
     a.wd = hp->wd;
     a.clip = hp->clip;
