@@ -425,6 +425,54 @@ def capture_step_graphs(pipe: Pipeline, hp: sf.AdamParams, status, token_buf: to
     return graphs
 
 
+class DensePlan:
+    """The dense tensors of a model (norm gains, biases, heads, adapters, experts' weights) and their AdamW
+    step: the argument array, the device step count and, with max_norm, the norm's workspace, built once.
+
+    tensors: sf.Dense holders or sf.dense_tensor() descriptors; hp: their hyper-parameters; max_norm > 0 clips the
+    global norm of their gradients; inv_scale undoes a loss scale. A step whose gradients are not finite is
+    skipped on the device (max_norm or inv_scale given)."""
+
+    def __init__(self, tensors, hp: sf.AdamParams, max_norm: float = 0.0, inv_scale: float = 1.0):
+        self.tensors = sf.DenseTensors(tensors)
+        self.hp, self.max_norm, self.inv_scale = hp, max_norm, inv_scale
+        device = hp.bc1.device
+        self.steps = sf.step_words(device)
+        self.with_norm = max_norm > 0.0 or inv_scale != 1.0
+        self.norm = torch.zeros(2, dtype=torch.float32, device=device)
+        self.ws = sf.grad_norm_workspace(self.tensors, device) if self.with_norm else None
+
+    def step(self, status=None, stream=None):
+        if self.with_norm:
+            sf.sf_grad_norm(self.tensors, self.norm, self.ws, self.max_norm, self.inv_scale, status, stream)
+        sf.sf_adamw_step(self.tensors, self.hp, self.steps, self.norm if self.with_norm else None, status, stream)
+
+
+class ExpertProjection:
+    """One projection of an expert layer: E weight matrices [R x C] as fp32 masters with their AdamW state and the
+    bf16 live copy that the products read, and an fp32 gradient. `dense` goes into a DensePlan, whose step writes
+    the live copy; tokens come sorted by expert, with the experts' offsets on the device."""
+
+    def __init__(self, W: torch.Tensor, state: int = sf.SF_TYPE_F32, decay: float = 1.0):
+        self.E, self.R, self.C = W.shape
+        self.grad = torch.zeros_like(W)
+        self.dense = sf.Dense(W, self.grad, state, live=True, decay=decay)
+
+    @property
+    def live(self) -> torch.Tensor:
+        return self.dense.live
+
+    def forward(self, A, Y, offsets, status=None, stream=None):
+        """Y[t] = W[e(t)] A[t]."""
+        sf.sf_grouped_forward(sf.grouped_problem(A, self.live, Y, offsets), status, stream)
+
+    def backward(self, A, dY, offsets, dA=None, accumulate: bool = False, status=None, stream=None):
+        """The weight gradient (added to the held one with accumulate) and, with dA, the input gradient."""
+        sf.sf_grouped_dw(sf.grouped_problem(A, self.grad, dY, offsets), status, stream, accumulate)
+        if dA is not None:
+            sf.sf_grouped_dx(sf.grouped_problem(dA, self.live, dY, offsets), status, stream)
+
+
 class Trainer:
     """The host loop around the step ("Sparse-First Fine-Tuning", sections 2.4-2.6).
 
@@ -432,13 +480,17 @@ class Trainer:
     read back in the middle of one), lets the rewind policy save or restore the active-row
     checkpoint, sets every pair's mix from the Helix schedule, and issues the step on `stream`,
     or skips it when the policy has just rewound. `pipes` are Pipeline objects over the same
-    model (e.g. one per input bank); step k uses pipes[k % len(pipes)]."""
+    model (e.g. one per input bank); step k uses pipes[k % len(pipes)]. `dense` (a DensePlan) is
+    stepped behind the sparse step, on the same stream, and left out with it."""
+
+    dense: DensePlan | None = None
 
     def __init__(self, model: SparseModel, pipes, hp: sf.AdamParams, status, stream=None,
-                 policy=None, helix=None, device=None):
+                 policy=None, helix=None, device=None, dense: DensePlan | None = None):
         from . import helix as hx
         self.model, self.pipes, self.hp, self.status = model, list(pipes), hp, status
         self.stream = stream
+        self.dense = dense
         self.helix = helix if helix is not None else hx.Helix()
         self.rewinder = hx.Rewinder(model.all_mats, policy or hx.RewindPolicy(), self.helix,
                                     device=device or model.device)
@@ -457,4 +509,6 @@ class Trainer:
         if tokens is not None:
             pipe.set_tokens(tokens)
         pipe.step(self.hp, st, stream)
+        if self.dense is not None:
+            self.dense.step(self.status, stream)
         return act
