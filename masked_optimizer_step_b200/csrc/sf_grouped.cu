@@ -27,7 +27,7 @@ constexpr int G_BOX_BYTES = 64 * GK * 2;      // a 64 x 64 box
 
 // ---- tiles of CTA pairs: 256 accumulator rows x up to 512 columns, both CTAs' MMAs as one (cta_group::2). The columns
 // are two halves of up to 256, two MMAs that share a stage's M operand: a stage of 48 KB in each SM then keeps the
-// tensor cores busy for 1,024 cycles, so 4 of them cover the 2 us that a stage takes from its release to its next use
+// tensor cores busy for 1,024 cycles, so the ring's 4 cover the 2 us that a stage takes from its release to its next use
 // (pairs of 256 x 256 with 32 KB stages: 512 cycles, and 1.4 us with nothing else on the memory system). ----
 constexpr int PM = 256;                       // accumulator rows of a pair, 128 in each CTA's TMEM
 constexpr int PN = 256;                       // columns of a half, at most
@@ -37,11 +37,11 @@ constexpr int P_EPI_WARPS = 8;                // two per TMEM lane quarter
 constexpr int P_THREADS = 64 + 32 * P_EPI_WARPS;
 constexpr int W_THREADS = P_THREADS + 32;     // weight gradient: and a warp that clears rows
 constexpr int T_TOKENS = 2 * PN;              // columns of a tile, at most
-constexpr int T_STAGES = 4;
-constexpr int T_STAGE_BYTES = 3 * P_HALF_BYTES;
+constexpr int T_RING_BYTES = 4 * 3 * P_HALF_BYTES;
+constexpr int T_MAX_STAGES = 8;
 constexpr int T_OUT_BYTES = 32 * 128 * 2;     // forward, dx: 32 tokens' rows of the CTA's 128 features, on their way out
 constexpr int W_OUT_BYTES = 32 * 128;         // weight gradient: 32 rows of 128 bytes of a warp's output
-constexpr size_t T_SMEM_BYTES = (size_t)T_STAGES * T_STAGE_BYTES + 2 * T_OUT_BYTES + 1024;
+constexpr size_t T_SMEM_BYTES = (size_t)T_RING_BYTES + 2 * T_OUT_BYTES + 1024;
 // weight gradient: 256 columns to a tile, two accumulators that the MMAs and the epilogue take in turn
 constexpr int W_STAGES_NEW = 6, W_STAGES_OLD = 3;
 constexpr int W_STAGE_BYTES = 2 * P_HALF_BYTES;
@@ -73,7 +73,7 @@ __device__ __forceinline__ int cand_tokens(int i) { return T_TOKENS - 32 * i; } 
 struct GArgs {
     CUtensorMap tm_w;          // forward, dx: W as {C, R, E}; dw: A as {C, T}
     CUtensorMap tm_x;          // tokens: forward A, dx Y as {K, T}; dw: Y as {R, T}
-    CUtensorMap tm_out;        // dw: W as {C, R, E}, boxes of 128 bytes x 32 rows
+    CUtensorMap tm_out;        // dw: W as {C, R, E}, boxes of 128 bytes x 32 rows; CTA pairs: tm_x with boxes half as high
     const int32_t *offsets;
     void *out;
     int64_t ld_out, stride_out;
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full_bar[T_STAGES], empty_bar[T_STAGES], tfull_bar[2], tempty_bar[2], drain_bar;
+    __shared__ uint64_t full_bar[T_MAX_STAGES], empty_bar[T_MAX_STAGES], tfull_bar[2], tempty_bar[2], drain_bar;
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile int abort_flag;
     __shared__ Plan pl;
@@ -309,7 +309,7 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 
     if (tid == 0) {
         abort_flag = 0;
-        for (int s = 0; s < T_STAGES; ++s) {
+        for (int s = 0; s < T_MAX_STAGES; ++s) {
             mbar_init(&full_bar[s], 1);
             mbar_init(&empty_bar[s], 1);
         }
@@ -321,12 +321,18 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         fence_mbarrier_init();
         prefetch_tmap(&g.tm_w);
         prefetch_tmap(&g.tm_x);
+        prefetch_tmap(&g.tm_out);
     }
     if (!load_offsets(pl, g.offsets, g.E, g.T)) {     // both CTAs of every pair see the same offsets
         if (blockIdx.x == 0 && tid == 0) set_status(status, SF_STATUS_BAD_OFFSET);
         return;
     }
     const int most = choose_tile(pl, g, workers);
+    // The ring's stages hold what the tiles need: 8 of 24 KB, 6 of 32 KB or 4 of 48 KB. Tiles of up to 128 tokens are
+    // bound by the requests to L2 (boxes asked for into L2 ahead of their loads cost 5 to 20% more time), so their token
+    // boxes are half as high: 16 experts of 2048 x 2048 over 2048 tokens 39.0 -> 35.7 us, 48 of 1416 x 2056 over 5000
+    // 77.6 -> 69.5 us, with an expert of half the tokens among them 90.7 -> 78.3 us.
+    const int stages = most <= 128 ? 8 : most <= PN ? 6 : 4, stage_bytes = T_RING_BYTES / stages;
     order_experts(pl, g.E, [&](int cnt) { return cnt > 0 ? tile_tokens(cnt, most, 32) : 0; });
     count_units(pl, g.E, [&](int cnt) { return cnt > 0 ? quot_up(cnt, tile_tokens(cnt, most, 32)) * ((g.M + PM - 1) / PM) : 0; });
     if (warp == 1) tmem_alloc_pair(&tmem_base_s, P_TMEM_COLS);
@@ -343,8 +349,8 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            bool issued[T_STAGES] = {};
-            uint32_t issued_parity[T_STAGES] = {};
+            uint32_t issued = 0;                  // a bit a stage
+            uint32_t issued_parity = 0;
             bool ok = true;
             for (int i = 0; i * workers < total_units && ok; ++i) {
                 const int u = unit_of(i, worker, workers);
@@ -352,10 +358,12 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                 const PUnit x = pair_unit(pl, g, most, u);
                 const int m = x.m0 + (int)crank * 128;
                 const int ta = x.t0 + (int)crank * (x.n0 / 2), tb = x.t0 + x.n0 + (int)crank * (x.n1 / 2);
-                const uint32_t bytes = 2 * (uint32_t)P_HALF_BYTES * (x.n1 ? 3 : 2);
+                const bool low = x.n0 <= 128;         // 64 rows of tokens to a CTA at most: the low box
+                const CUtensorMap *tx = low ? &g.tm_out : &g.tm_x;
+                const uint32_t bytes = (uint32_t)P_HALF_BYTES * (low ? 3 : x.n1 ? 6 : 4);
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag)) { ok = false; break; }
-                    uint8_t *sw = smem + stage * T_STAGE_BYTES, *sx = sw + P_HALF_BYTES;
+                    uint8_t *sw = smem + stage * stage_bytes, *sx = sw + P_HALF_BYTES;
                     if (leader) mbar_arrive_expect_tx(&full_bar[stage], bytes);
                     if (TRANS) {
                         tma_load_3d_pair(sw, &g.tm_w, &full_bar[stage], m, kb * GK, x.e);
@@ -363,11 +371,11 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                     } else {
                         tma_load_3d_pair(sw, &g.tm_w, &full_bar[stage], kb * GK, m, x.e);
                     }
-                    tma_load_2d_pair(sx, &g.tm_x, &full_bar[stage], kb * GK, ta);
+                    tma_load_2d_pair(sx, tx, &full_bar[stage], kb * GK, ta);
                     if (x.n1) tma_load_2d_pair(sx + P_HALF_BYTES, &g.tm_x, &full_bar[stage], kb * GK, tb);
-                    issued[stage] = true;
-                    issued_parity[stage] = phase;
-                    if (++stage == T_STAGES) { stage = 0; phase ^= 1u; }
+                    issued |= 1u << stage;
+                    issued_parity = (issued_parity & ~(1u << stage)) | phase << stage;
+                    if (++stage == stages) { stage = 0; phase ^= 1u; }
                 }
             }
             {   // the MMA issuer commits drain_bar once it has finished or given up
@@ -375,10 +383,10 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                 while (!mbar_try_wait(&drain_bar, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
             }
             if ((!ok || abort_flag) && leader) {  // both CTAs' loads complete on the leader's barriers
-                for (int s = 0; s < T_STAGES; ++s) {
-                    if (!issued[s]) continue;
+                for (int s = 0; s < stages; ++s) {
+                    if (!(issued >> s & 1u)) continue;
                     const uint64_t t0 = globaltimer_ns();
-                    while (!mbar_try_wait(&full_bar[s], issued_parity[s]) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+                    while (!mbar_try_wait(&full_bar[s], issued_parity >> s & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {}
                 }
             }
         }
@@ -392,8 +400,8 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
             const uint64_t w0 = TRANS ? mnmajor(s0) : kmajor(s0), x0 = kmajor(s0 + P_HALF_BYTES);
             // one half's MMAs of a stage: 16 of K are 32 bytes of a K-major row, or 16 rows of 128 bytes
             auto half_stage = [&](int h, int st, uint32_t id, bool first, bool last, bool release) {
-                const uint64_t dw = w0 + (uint64_t)(st * (T_STAGE_BYTES >> 4));
-                const uint64_t dx = x0 + (uint64_t)(st * (T_STAGE_BYTES >> 4) + h * (P_HALF_BYTES >> 4));
+                const uint64_t dw = w0 + (uint64_t)(st * (stage_bytes >> 4));
+                const uint64_t dx = x0 + (uint64_t)(st * (stage_bytes >> 4) + h * (P_HALF_BYTES >> 4));
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < GK / G_UMMA_K; ++k)
@@ -415,8 +423,8 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                 const int ahead = x.n1 ? min(T_AHEAD, nk) : 0;
                 int kb = 0;
                 for (; kb < ahead && ok; ++kb) {
-                    const int st = stage + kb < T_STAGES ? stage + kb : stage + kb - T_STAGES;
-                    const uint32_t ph = stage + kb < T_STAGES ? phase : phase ^ 1u;
+                    const int st = stage + kb < stages ? stage + kb : stage + kb - stages;
+                    const uint32_t ph = stage + kb < stages ? phase : phase ^ 1u;
                     ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[st], ph, &abort_flag));
                     if (!ok) break;
                     tc_fence_after();
@@ -427,7 +435,7 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                 tc_fence_after();
                 for (kb = 0; kb < ahead; ++kb) {
                     half_stage(1, stage, id1, kb == 0, kb == nk - 1, true);
-                    if (++stage == T_STAGES) { stage = 0; phase ^= 1u; }
+                    if (++stage == stages) { stage = 0; phase ^= 1u; }
                 }
                 for (; kb < nk; ++kb) {
                     ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, &abort_flag));
@@ -435,7 +443,7 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                     tc_fence_after();
                     half_stage(0, stage, id0, kb == 0, kb == nk - 1, x.n1 == 0);
                     if (x.n1) half_stage(1, stage, id1, false, kb == nk - 1, true);
-                    if (++stage == T_STAGES) { stage = 0; phase ^= 1u; }
+                    if (++stage == stages) { stage = 0; phase ^= 1u; }
                 }
                 half_phase ^= x.n1 ? 3u : 1u;
             }
@@ -448,7 +456,7 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         // --------------------------- epilogue (warps 2..9) ---------------------------
         const int quad = warp & 3;              // TMEM lanes 32*quad .. 32*quad+31
         const int part = (warp - 2) >> 2;       // 128 of a half's columns
-        uint8_t *s_out = smem + T_STAGES * T_STAGE_BYTES + part * T_OUT_BYTES;
+        uint8_t *s_out = smem + T_RING_BYTES + part * T_OUT_BYTES;
         uint32_t half_phase = 0;
         bool ready = true;
         for (int i = 0; i * workers < total_units && ready; ++i) {
@@ -1623,7 +1631,8 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
 
     if (!one_round && p->T > (int64_t)SF_GROUPED_PAIR_FROM * p->E) {
         if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, w_rows) ||
-            !encode(&g.tm_x, p->type, x, g.K, p->T, ld_x, 0, 0, 128))
+            !encode(&g.tm_x, p->type, x, g.K, p->T, ld_x, 0, 0, 128) ||
+            !encode(&g.tm_out, p->type, x, g.K, p->T, ld_x, 0, 0, 64))
             return SF_ERR_CUDA;
         const int slots = pair_slots();
         if (slots <= 0) return SF_ERR_CUDA;
