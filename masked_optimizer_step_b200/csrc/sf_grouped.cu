@@ -323,6 +323,7 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         prefetch_tmap(&g.tm_x);
         prefetch_tmap(&g.tm_out);
     }
+    griddep_wait();                             // what the launches before this one wrote is there from here on
     if (!load_offsets(pl, g.offsets, g.E, g.T)) {     // both CTAs of every pair see the same offsets
         if (blockIdx.x == 0 && tid == 0) set_status(status, SF_STATUS_BAD_OFFSET);
         return;
@@ -378,6 +379,7 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                     if (++stage == stages) { stage = 0; phase ^= 1u; }
                 }
             }
+            griddep_launch_dependents();        // the next launch may take what room is left
             {   // the MMA issuer commits drain_bar once it has finished or given up
                 const uint64_t t0 = globaltimer_ns();
                 while (!mbar_try_wait(&drain_bar, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
@@ -872,6 +874,7 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         prefetch_tmap(&g.tm_x);
         prefetch_tmap(&g.tm_out);
     }
+    griddep_wait();                             // what the launches before this one wrote is there from here on
     int busy = 0;                               // experts with tokens
     {   // offsets: valid, and the experts' order
         int bad = 0, some = 0;
@@ -949,6 +952,7 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                     if (++stage == W_STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
+            griddep_launch_dependents();
             {
                 const uint64_t t0 = globaltimer_ns();
                 while (!mbar_try_wait(&drain_bar, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
@@ -1562,25 +1566,22 @@ int launch(K kernel, int grid, int cluster, int threads, size_t smem, const GArg
 {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return SF_ERR_CUDA;
-    cudaLaunchAttribute attr;
-    if (cluster > 1) {
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = cluster;
-        attr.val.clusterDim.y = 1;
-        attr.val.clusterDim.z = 1;
-    } else {
-        // programmatic dependent launch: the small kernels wait for their predecessor themselves, behind what they can
-        // do without it (4.4 -> 3.4 us for the smallest calls back to back)
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-    }
+    // programmatic dependent launch: the kernels wait for their predecessor themselves, behind what they can do without it
+    // (4.4 -> 3.4 us for the smallest calls back to back)
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = as_stream(stream);
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kernel, g, status) != cudaSuccess) return SF_ERR_CUDA;
     return launch_status();
 }
