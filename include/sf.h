@@ -403,9 +403,9 @@ int sf_masked_dw_phase(const sf_dw_problem *probs /* host [n] */, int n, void *w
  * finite) the step is skipped: every tensor and the step count stay as they are, and
  * SF_STATUS_NONFINITE is set. A step that produces a non-finite weight or moment sets it too.
  *
- * sf_grad_norm: out[0] = inv_scale * sqrt(sum of squares of every gradient of every tensor) (squares
- * in fp32, sums in fp64, in a fixed order), out[1] = inv_scale * min(1, max_norm / (out[0] + 1e-6)),
- * or inv_scale when max_norm <= 0; out[1] = 0 (and SF_STATUS_NONFINITE) when the norm is not finite.
+ * sf_grad_norm: out[0] = inv_scale * sqrt(sum of squares of every gradient of every tensor) (the squares
+ * of eight elements summed in fp32, from there in fp64, in a fixed order), out[1] =
+ * inv_scale * min(1, max_norm / (out[0] + 1e-6)), or inv_scale when max_norm <= 0; out[1] = 0 (and SF_STATUS_NONFINITE) when the norm is not finite.
  * inv_scale undoes a loss scale (1 for none). Only n, g and g_type of a tensor are read. ws:
  * sf_grad_norm_ws_bytes() bytes, 16-byte aligned, zeroed once by the caller; every call leaves it
  * ready for the next. Calls that can overlap need workspaces of their own.
@@ -458,8 +458,9 @@ int sf_adamw_step(const sf_dense *t /* host [n] */, int n, const sf_adam *hp, in
  * results whose sums hold it.
  * offsets must not fall and must lie in [0, T]: otherwise nothing is computed and SF_STATUS_BAD_OFFSET is
  * set. Pipeline waits are bounded as in sf_masked_dw (SF_STATUS_WAIT_TIMEOUT).
- * Deterministic: every result is summed by one CTA (or by a cluster in a fixed order), and which rows
- * share a tile changes no sum. Requirements: 1 <= E <= 1024; T >= 0; R, C positive multiples of 8;
+ * Deterministic: every result is summed by one CTA or pair of CTAs in an order that the sizes and, for the
+ * weight gradient, the expert's tokens give; which rows share a tile changes no sum. The written operand
+ * must not overlap the others (one address for two operands is refused). Requirements: 1 <= E <= 1024; T >= 0; R, C positive multiples of 8;
  * ld_a >= C, ld_y >= R, ld_w >= C, stride_w >= (R - 1) * ld_w + C when E > 1; strides multiples of 8 elements
  * (4 for an fp32 W); A, W, Y 16-byte aligned (A and Y may be NULL when T = 0). One launch a call.
  * Errors: SF_ERR_ARG, SF_ERR_ALIGN, SF_ERR_UNSUPPORTED (E above 1024, or more than 2^30 tiles).

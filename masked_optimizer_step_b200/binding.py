@@ -458,10 +458,10 @@ def _type(t, allowed, what) -> int:
 
 
 def _one_device(*tensors) -> int:
-    """The index of the GPU that all the given tensors (None among them) are on."""
+    """The index of the GPU that all the given tensors (None and addresses among them) are on."""
     index = -1
     for t in tensors:
-        if t is None:
+        if t is None or isinstance(t, int):
             continue
         d = t.get_device()
         if d < 0 or (index >= 0 and d != index):
@@ -470,6 +470,11 @@ def _one_device(*tensors) -> int:
     if index < 0:
         raise ValueError("device tensors on one GPU expected")
     return index
+
+
+def _status_ptr(status) -> int | None:
+    """A status word's address: a device tensor's, or the address itself, as Pipeline and Trainer pass it on."""
+    return status if isinstance(status, int) else _ptr(status)
 
 
 def _on_current(index: int):
@@ -548,6 +553,9 @@ class DenseTensors:
         self.anchor = self.descs[0].refs[0] if self.n else None
         if self.n:
             _one_device(*[t for d in self.descs for t in d.refs])
+        written = [t.data_ptr() for d in self.descs for k, t in enumerate(d.refs) if k != 1 and t is not None and t.numel()]
+        if len(set(written)) != len(written):
+            raise ValueError("a tensor is in the list twice, or shares its weights or state with another")
 
 
 def step_words(device=None) -> torch.Tensor:
@@ -572,7 +580,7 @@ def sf_grad_norm(tensors: DenseTensors, out, ws, max_norm: float = 0.0, inv_scal
     index = _one_device(tensors.anchor, out, ws, status)
     _on_current(index)
     _check(load().sf_grad_norm(tensors.arr, tensors.n, inv_scale, max_norm, _ptr(out), _ptr(ws),
-                               ws.numel() * ws.element_size(), _ptr(status), _stream_on(index, stream)), "sf_grad_norm")
+                               ws.numel() * ws.element_size(), _status_ptr(status), _stream_on(index, stream)), "sf_grad_norm")
 
 
 def sf_adamw_step(tensors: DenseTensors, hp: AdamParams, step, factor=None, status=None, stream=None):
@@ -583,7 +591,7 @@ def sf_adamw_step(tensors: DenseTensors, hp: AdamParams, step, factor=None, stat
     index = _one_device(tensors.anchor, step, factor, status, hp.bc1)
     _on_current(index)
     h = hp.struct()
-    _check(load().sf_adamw_step(tensors.arr, tensors.n, ctypes.byref(h), _ptr(step), _ptr(factor), _ptr(status),
+    _check(load().sf_adamw_step(tensors.arr, tensors.n, ctypes.byref(h), _ptr(step), _ptr(factor), _status_ptr(status),
                                 _stream_on(index, stream)), "sf_adamw_step")
 
 
@@ -612,9 +620,9 @@ def grouped_problem(A, W, Y, offsets) -> Desc:
     _type(Y, (ty,), "Y")
     _one_device(A, W, Y, offsets)
     # a single row's or matrix's stride says nothing: give the dense one
-    ld_a = A.stride(0) if T > 1 else max(A.stride(0), C)
-    ld_y = Y.stride(0) if T > 1 else max(Y.stride(0), R)
-    ld_w = W.stride(1) if R > 1 else max(W.stride(1), C)
+    ld_a = A.stride(0) if T > 1 else C
+    ld_y = Y.stride(0) if T > 1 else R
+    ld_w = W.stride(1) if R > 1 else C
     stride_w = W.stride(0) if E > 1 else R * ld_w
     c = sf_grouped(_ptr(A) or None, ld_a, _ptr(W), ld_w, stride_w, _ptr(Y) or None, ld_y, _ptr(offsets), E, T, R, C,
                    ty, wt)
@@ -624,7 +632,7 @@ def grouped_problem(A, W, Y, offsets) -> Desc:
 def _grouped(name, p: Desc, status, stream, *extra):
     index = _one_device(p.refs[1], status)
     _on_current(index)
-    _check(getattr(load(), name)(ctypes.byref(p.c), *extra, _ptr(status), _stream_on(index, stream)), name)
+    _check(getattr(load(), name)(ctypes.byref(p.c), *extra, _status_ptr(status), _stream_on(index, stream)), name)
 
 
 def sf_grouped_forward(p: Desc, status=None, stream=None):

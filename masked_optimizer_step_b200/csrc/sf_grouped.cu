@@ -60,7 +60,6 @@ constexpr int D_THREADS = P_THREADS;          // weight gradient: TMA, MMA and e
 constexpr int D_STAGE_BYTES = 3 * P_HALF_BYTES;
 constexpr int D_MAX_STAGES = 4;
 
-
 // Weight gradient, fp32: tokens that the tensor core sums before the sums are added in fp32, in stages. It adds with
 // truncation, so the error grows with the length (relative, normal values: 2.3e-7, 9.9e-7 and 9.1e-6 at 256, 1,024
 // and 8,192 tokens); 960 keep it below 1e-6 at any length.
@@ -830,10 +829,14 @@ __device__ __forceinline__ WUnit dw_unit(const WPlan &pl, const GArgs &g, int u)
 
 __device__ __forceinline__ bool has_tail(const WUnit &x) { return (x.cnt & (G_UMMA_K - 1)) != 0; }
 
+// A pair sums 256 x 256 of W[e] over chunks of 960 tokens at most, in two accumulators in turn; the epilogue warps add the
+// chunks' sums in registers. What bounds it is the traffic between L2 and the SMs: 64 KB a stage and pair, 10.3 TB/s into
+// the SMs and 12.7 TB/s in all with the tensor cores 72% active (4 experts of 4096 x 4096 over 2,048 tokens each; the
+// forward kernel's 512-column tiles take a quarter less and keep them 82% active). Wider tiles have no place for the sums:
+// 256 x 512 of fp32 are an SM pair's whole register files.
 // OLD: for gradients that are added to, over few tokens. What W holds comes into the output boxes by TMA while the MMAs
 // run, is added there and goes out by TMA: the time is that of reading and writing W once, with fewer stages for the
-// tokens and a place for all of a warp's boxes. Otherwise the addition is TMA's, at 2.4 TB/s of results: 321 us against
-// 392 .. (see the launch) where the tokens take longer than W.
+// tokens and a place for all of a warp's boxes. Otherwise the addition is TMA's, at 2.4 TB/s of results.
 template <bool OLD>
 __global__ void __launch_bounds__(W_THREADS, 1)
 grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
@@ -1524,6 +1527,7 @@ int check_grouped(const sf_grouped *p, bool dw)
     const int64_t tall = (int64_t)p->T / 16 + p->E;
     if (wide * tall > (1 << 30) || (int64_t)p->E * ((p->R + PM - 1) / PM) * ((p->C + 63) / 64) > (1 << 30))
         return SF_ERR_UNSUPPORTED;
+    if (p->T > 0 && (p->A == p->Y || p->A == p->W || p->Y == p->W)) return SF_ERR_ARG;      // one is written
     return SF_OK;
 }
 
@@ -1586,13 +1590,16 @@ int launch(K kernel, int grid, int cluster, int threads, size_t smem, const GArg
     return launch_status();
 }
 
-// Pairs run when an expert has more than this many tokens on average.
-#ifndef SF_GROUPED_PAIR_FROM
-#define SF_GROUPED_PAIR_FROM 96
-#endif
-#ifndef SF_GROUPED_DW_OLD_BELOW
-#define SF_GROUPED_DW_OLD_BELOW 512
-#endif
+// Forward, dx: pairs run when an expert has more than this many tokens on average. At 96, 128 and 256 of them, single CTAs
+// against pairs: 50.6 / 64.5, 70.6 / 65.9 and 98 / 76 us for 8 experts of 4096 x 4096; 69.8 / 74.4, 96 / 79 and 158 / 101 us
+// for 48 of 1416 x 2056; 258 / 299, 308 / 340 and 455 / 369 us for 16 of 11008 x 4096. With short sums they cross later
+// (64 experts of 1024 x 1024: 32 / 44, 37 / 46, 52 / 56 us), with unevenly filled experts sooner (48 of 1416 x 2056 over 96
+// tokens each on average: 88 / 66 us).
+constexpr int64_t kPairFrom = 96;
+// dw that adds: below this many tokens to an expert, what W holds comes in by TMA and is added in shared memory; from there
+// on the addition is TMA's. 4 experts of 11008 x 4096 over 64, 256, 512 and 900 tokens each: 250, 259, 313 and 509 us the
+// one way, 322, 327, 330 and 418 us the other.
+constexpr int64_t kDwOldBelow = 512;
 
 template <bool TRANS>
 int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
@@ -1630,7 +1637,7 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
     const int64_t m_tiles = (g.M + SM_ROWS - 1) / SM_ROWS;
     const bool one_round = tiles * m_tiles <= 2 * sms;
 
-    if (!one_round && p->T > (int64_t)SF_GROUPED_PAIR_FROM * p->E) {
+    if (!one_round && p->T > kPairFrom * p->E) {
         if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, w_rows) ||
             !encode(&g.tm_x, p->type, x, g.K, p->T, ld_x, 0, 0, 128) ||
             !encode(&g.tm_out, p->type, x, g.K, p->T, ld_x, 0, 0, 64))
@@ -1716,7 +1723,7 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
             return SF_ERR_CUDA;
         const int slots = pair_slots();
         if (slots <= 0) return SF_ERR_CUDA;
-        const bool old = accumulate && p->T < (int64_t)SF_GROUPED_DW_OLD_BELOW * p->E;
+        const bool old = accumulate && p->T < kDwOldBelow * p->E;
         return launch(old ? grouped_dw_kernel<true> : grouped_dw_kernel<false>,
                       2 * (int)(pair_units < slots ? pair_units : slots), 2, W_THREADS, W_SMEM_BYTES, g, dev_status, stream);
     }

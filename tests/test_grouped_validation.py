@@ -78,6 +78,13 @@ def test_16bit_gradients_are_not_accumulated(lib):
     assert lib.sf_grouped_dw(ctypes.byref(p), 1, None, None) == ARG
 
 
+@pytest.mark.parametrize("call", ["sf_grouped_forward", "sf_grouped_dx", "sf_grouped_dw"])
+@pytest.mark.parametrize("same", [dict(Y=P, W=P + 16), dict(W=P, Y=P + 16), dict(W=P + 16, Y=P + 16)])
+def test_operands_do_not_share_an_address(lib, call, same):
+    extra = (0,) if call == "sf_grouped_dw" else ()
+    assert getattr(lib, call)(ctypes.byref(_problem(**same)), *extra, None, None) == ARG
+
+
 def test_null_problem(lib):
     assert lib.sf_grouped_forward(None, None, None) == ARG
     assert lib.sf_grouped_dx(None, None, None) == ARG
