@@ -540,7 +540,8 @@ class Dense:
         self.live = p.to(torch.bfloat16) if live else None
 
     def desc(self) -> Desc:
-        return dense_tensor(self.p, self.g, self.m, self.v, self.live, self.decay, self.m_scale, self.v_scale)
+        live = None if self.live is self.p else self.live            # bf16 weights are their own live copy
+        return dense_tensor(self.p, self.g, self.m, self.v, live, self.decay, self.m_scale, self.v_scale)
 
 
 class DenseTensors:
