@@ -7,8 +7,8 @@
 // Layout of the work: a block of 256 elements (the unit that shares the 8-bit moments' scales) belongs to
 // one warp, 8 consecutive elements to a lane, so every access is an 8-, 16- or 32-byte vector of a
 // fully coalesced row and a block's largest magnitude is one warp-wide integer maximum. A unit is
-// `per` blocks for each of a CTA's 8 warps; units of all tensors are numbered through and a CTA
-// takes every gridDim-th one.
+// `per` blocks for each of a CTA's 8 warps; units of all tensors are numbered through. A CTA of the
+// step takes one, a CTA of the norm every gridDim-th one.
 #include <string.h>
 
 #include <cuda_fp8.h>
@@ -283,30 +283,33 @@ __device__ __forceinline__ float encode8(const pair_t (&x)[4], void *base, int64
     return sc;
 }
 
-// A warp's way through the blocks of its CTA's units.
-template <int N>
-struct Cursor {
-    const DenseBatch<N> &b;
-    int unit, which, k;        // unit, its tensor, block of the unit
-    int64_t blk;               // block of the tensor
+// A warp's way through its blocks of the CTA's unit, kWarps apart. The tensor comes from the CTA's number alone, so its
+// description stays in uniform registers; only the warp's place in it is each lane's own (with the place worked out anew
+// for each block the step took 502 instructions a block).
+constexpr int kStride = kWarps * kBlock;
 
-    __device__ __forceinline__ Cursor(const DenseBatch<N> &batch) : b(batch), unit((int)blockIdx.x - (int)gridDim.x), which(0), k(batch.per), blk(0)
+struct Place {
+    int64_t at;                // this lane's first element
+    int64_t blk;               // block of the tensor
+    int left;                  // elements from the block's first one on, 2^30 at most
+    int more;                  // blocks from here on
+
+    __device__ __forceinline__ Place(const DenseDesc &d, int unit, int per)
     {
-        next();
+        blk = (int64_t)unit * per * kWarps + (threadIdx.x >> 5);
+        at = blk * kBlock + (threadIdx.x & 31) * kLaneElems;
+        left = (int)max((int64_t)0, min(d.n - blk * kBlock, (int64_t)1 << 30));
+        more = min(per, (left + kStride - 1) / kStride);
     }
-    __device__ __forceinline__ bool there() const { return unit < b.units; }
     __device__ __forceinline__ void next()
     {
-        ++k;
+        at += kStride;
         blk += kWarps;
-        while (k >= b.per || blk * kBlock >= b.d[which].n) {
-            unit += gridDim.x;
-            if (unit >= b.units) return;
-            which = find_tensor(b, unit);
-            k = 0;
-            blk = (int64_t)(unit - b.unit_begin[which]) * b.per * kWarps + (threadIdx.x >> 5);
-        }
+        left -= kStride;
+        --more;
     }
+    __device__ __forceinline__ bool full() const { return left >= kBlock; }
+    __device__ __forceinline__ int count() const { return max(0, min(8, left - (int)(threadIdx.x & 31) * kLaneElems)); }
 };
 
 // What a block's step reads, as it lies in memory.
@@ -314,42 +317,49 @@ template <bool CODED>
 struct Block {
     Raw8 p, g, m, v;           // moments: fp32
     uint2 cm, cv;              // or codes
-    float sm, sv;              // and their scales
 
-    __device__ __forceinline__ void load(const DenseDesc &d, int64_t blk, int lane)
+    __device__ __forceinline__ void load(const DenseDesc &d, const Place &w)
     {
-        const int64_t at = blk * kBlock + lane * kLaneElems;
-        if ((blk + 1) * kBlock <= d.n) load_from<true>(d, blk, at, 8);
-        else load_from<false>(d, blk, at, (int)max((int64_t)0, min((int64_t)8, d.n - at)));
+        if (w.full()) load_from<true>(d, w, 8);
+        else load_from<false>(d, w, w.count());
     }
     template <bool FULL>
-    __device__ __forceinline__ void load_from(const DenseDesc &d, int64_t blk, int64_t at, int cnt)
+    __device__ __forceinline__ void load_from(const DenseDesc &d, const Place &w, int cnt)
     {
-        p = load_raw<FULL>(d.p, d.p_type, at, cnt);
-        g = load_raw<FULL>(d.g, d.g_type, at, cnt);
+        p = load_raw<FULL>(d.p, d.p_type, w.at, cnt);
+        g = load_raw<FULL>(d.g, d.g_type, w.at, cnt);
         if (CODED) {
-            cm = load8_codes<FULL>(d.m, at, cnt);
-            cv = load8_codes<FULL>(d.v, at, cnt);
-            sm = d.m_scale[blk];
-            sv = d.v_scale[blk];
+            cm = load8_codes<FULL>(d.m, w.at, cnt);
+            cv = load8_codes<FULL>(d.v, w.at, cnt);
         } else {
-            m = load_raw<FULL>(d.m, SF_TYPE_F32, at, cnt);
-            v = load_raw<FULL>(d.v, SF_TYPE_F32, at, cnt);
+            m = load_raw<FULL>(d.m, SF_TYPE_F32, w.at, cnt);
+            v = load_raw<FULL>(d.v, SF_TYPE_F32, w.at, cnt);
         }
     }
 };
 
-// The lines of block `blk` into L2, ahead of its loads: a lane to a line of 128 bytes, 8 for an array of 32-bit values,
-// 4 of 16, 2 of 8.
-__device__ __forceinline__ void prefetch_block(const DenseDesc &d, int64_t blk, int lane)
-{
-    const int p_size = d.p_type == SF_TYPE_F32 ? 4 : 2, g_size = d.g_type == SF_TYPE_F32 ? 4 : 2;
-    const char *base = static_cast<const char *>(lane < 8 ? d.p : lane < 16 ? d.g : lane < 24 ? d.m : d.v);
-    const int s_size = d.state_type == SF_TYPE_F32 ? 4 : 1;
-    const int size = lane < 8 ? p_size : lane < 16 ? g_size : s_size, line = lane & 7;
-    const int64_t off = blk * kBlock * size + line * 128;
-    if (line < 2 * size && off < d.n * size) prefetch_l2(base + off);
-}
+// A block's lines into L2, ahead of its loads: a lane to a line of 128 bytes, 8 for an array of 32-bit values, 4 of 16, 2
+// of 8.
+struct Ahead {
+    const char *line;          // this lane's line of the next block asked for
+    int step, from;            // bytes from block to block; the line's first element in its block, 2^30 where there is none
+
+    __device__ __forceinline__ Ahead(const DenseDesc &d, const Place &w)
+    {
+        const int lane = threadIdx.x & 31, type = lane < 8 ? d.p_type : lane < 16 ? d.g_type : d.state_type;
+        const char *base = static_cast<const char *>(lane < 8 ? d.p : lane < 16 ? d.g : lane < 24 ? d.m : d.v);
+        const int size = type == SF_TYPE_F32 ? 4 : type == SF_TYPE_E4M3 ? 1 : 2, l = lane & 7;
+        line = base + w.blk * kBlock * size + l * 128;
+        step = kStride * size;
+        from = l < 2 * size ? l * 128 / size : 1 << 30;
+    }
+    // for the block that has `left` elements from its first one on
+    __device__ __forceinline__ void ask(int left)
+    {
+        if (from < left) prefetch_l2(line);
+        line += step;
+    }
+};
 
 struct StepNow {
     pair_t bc1, root_bc2, factor;
@@ -357,17 +367,16 @@ struct StepNow {
 
 // One block's step on what was loaded: this lane's eight elements. FULL: the block has all its 256.
 template <bool CODED, bool FULL>
-__device__ __forceinline__ void step_block(const Block<CODED> &in, const DenseDesc &d, int64_t blk, const StepArgs &a, const StepNow &now,
-                                           int lane, pair_t &nan_sum)
+__device__ __forceinline__ void step_block(const Block<CODED> &in, float sm, float sv, const DenseDesc &d, int64_t at, int64_t blk, int cnt,
+                                           const StepArgs &a, const StepNow &now, pair_t &nan_sum)
 {
-    const int64_t at = blk * kBlock + lane * kLaneElems;
-    const int cnt = FULL ? 8 : (int)max((int64_t)0, min((int64_t)8, d.n - at));
+    const int lane = threadIdx.x & 31;
     pair_t p[4], g[4], m[4], v[4];
     to_pairs(p, in.p, d.p_type);
     to_pairs(g, in.g, d.g_type);
     if (CODED) {
-        decode8(m, in.cm, in.sm);
-        decode8(v, in.cv, in.sv);
+        decode8(m, in.cm, sm);
+        decode8(v, in.cv, sv);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], v[e]);
     } else {
@@ -406,9 +415,9 @@ __device__ __forceinline__ void step_block(const Block<CODED> &in, const DenseDe
     else store8_bf16<FULL>(static_cast<uint16_t *>(d.p) + at, p, cnt);
     if (d.live) store8_bf16<FULL>(d.live + at, p, cnt);
     if (CODED) {                                     // a scale is the largest moment's: not finite where one of them is not
-        const float sm = encode8<FULL, false>(m, d.m, at, cnt, d.m_scale + blk, lane);
-        const float sv = encode8<FULL, true>(v, d.v, at, cnt, d.v_scale + blk, lane);
-        nan_sum = fma2(pair_of(sm, sv), zero, nan_sum);
+        const float new_sm = encode8<FULL, false>(m, d.m, at, cnt, d.m_scale + blk, lane);
+        const float new_sv = encode8<FULL, true>(v, d.v, at, cnt, d.v_scale + blk, lane);
+        nan_sum = fma2(pair_of(new_sm, new_sv), zero, nan_sum);
     } else {
         store8_f32<FULL>(static_cast<float *>(d.m) + at, m, cnt);
         store8_f32<FULL>(static_cast<float *>(d.v) + at, v, cnt);
@@ -416,19 +425,28 @@ __device__ __forceinline__ void step_block(const Block<CODED> &in, const DenseDe
 }
 
 // With fp32 moments a block's loads (3.5 KB a warp) are issued behind the stores of the block before. With 8-bit moments
-// they are 2 KB and the instructions take most of the memory's time, so four CTAs to an SM hide one another's waits: a
-// block is loaded where it is used, and its lines are asked for in L2 one block ahead.
+// they are 2 KB and the instructions (400 a block) take most of the memory's time, so four CTAs to an SM hide one another's
+// waits: a block is loaded where it is used, its lines are asked for in L2 one block ahead, and the scales, which those
+// lines leave out, are fetched for the whole unit at its beginning (2^26 elements over fp32 weights: 176 us, 203 with the
+// scales loaded block by block, 6.1 TB/s against 5.3).
 template <int N, bool CODED>
 __global__ void __launch_bounds__(kThreads, CODED ? 4 : 3)
 adamw_kernel(const __grid_constant__ DenseBatch<N> b, const __grid_constant__ StepArgs a, uint32_t *status)
 {
-    const int lane = threadIdx.x & 31;
-    Cursor<N> at(b);
+    const int lane = threadIdx.x & 31, which = find_tensor(b, blockIdx.x);
+    const DenseDesc &d = b.d[which];
+    Place w(d, blockIdx.x - b.unit_begin[which], b.per);
+    Ahead ahead(d, w);
     Block<CODED> in;
     griddep_wait();                                  // what the launches before this one wrote is there from here on
-    if (at.there()) {                                // before the step's own words, which take two trips to memory
-        if (CODED) prefetch_block(b.d[at.which], at.blk, lane);
-        else in.load(b.d[at.which], at.blk, lane);
+    float sms = 0.0f, svs = 0.0f;                    // 8-bit moments: lane k has the scales of the warp's k-th block
+    if (CODED && lane < w.more) {
+        sms = d.m_scale[w.blk + lane * kWarps];
+        svs = d.v_scale[w.blk + lane * kWarps];
+    }
+    if (w.more > 0) {                                // before the step's own words, which take two trips to memory
+        if (CODED) ahead.ask(w.left);
+        else in.load(d, w);
     }
     const int t = a.step[0] + 1;
     const float f = a.factor ? a.factor[1] : 1.0f;
@@ -441,15 +459,19 @@ adamw_kernel(const __grid_constant__ DenseBatch<N> b, const __grid_constant__ St
     const StepNow now = {pair_of(bc1, bc1), pair_of(root, root), pair_of(f, f)};
     pair_t nan_sum = pair_of(0.0f, 0.0f);            // stays 0 while everything is finite
 
-    while (at.there()) {
-        const DenseDesc &d = b.d[at.which];
-        const int64_t blk = at.blk;
-        at.next();
-        if (CODED && at.there()) prefetch_block(b.d[at.which], at.blk, lane);
-        if (CODED) in.load(d, blk, lane);
-        if ((blk + 1) * kBlock <= d.n) step_block<CODED, true>(in, d, blk, a, now, lane, nan_sum);
-        else step_block<CODED, false>(in, d, blk, a, now, lane, nan_sum);
-        if (!CODED && at.there()) in.load(b.d[at.which], at.blk, lane);
+    for (int k = 0; w.more > 0; ++k) {
+        const int64_t at = w.at, blk = w.blk;
+        const bool full = w.full();
+        const int cnt = w.count();
+        if (CODED) {
+            if (w.more > 1) ahead.ask(w.left - kStride);
+            in.load(d, w);
+        }
+        w.next();
+        const float sm = CODED ? __shfl_sync(0xffffffffu, sms, k) : 0.0f, sv = CODED ? __shfl_sync(0xffffffffu, svs, k) : 0.0f;
+        if (full) step_block<CODED, true>(in, sm, sv, d, at, blk, 8, a, now, nan_sum);
+        else step_block<CODED, false>(in, sm, sv, d, at, blk, cnt, a, now, nan_sum);
+        if (!CODED && w.more > 0) in.load(d, w);
     }
     griddep_launch_dependents();                     // the launch behind this one may take what room is left
     const float2 bad = halves(nan_sum);
@@ -494,12 +516,11 @@ grad_norm_kernel(const __grid_constant__ DenseBatch<N> b, int32_t *done, double 
         const int which = find_tensor(b, unit);
         const DenseDesc &d = b.d[which];
         const int64_t first = ((int64_t)(unit - b.unit_begin[which]) * b.per * kWarps + warp) * kBlock + lane * kLaneElems;
-        constexpr int64_t kStride = (int64_t)kWarps * kBlock;
         for (int k = 0; k < b.per; k += 4) {        // four blocks' loads at once
             Raw8 r[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int64_t at = first + (k + q) * kStride;
+                const int64_t at = first + (int64_t)(k + q) * kStride;
                 const int cnt = k + q < b.per ? (int)max((int64_t)0, min((int64_t)8, d.n - at)) : 0;
                 r[q] = load_raw<false>(d.g, d.g_type, at, cnt);
             }
@@ -574,14 +595,18 @@ int check_dense(const sf_dense *t, int n, bool step)
     return SF_OK;
 }
 
-// Blocks of a unit per warp: what makes one round of four CTAs to an SM of a small call, and 8 at most (a 7B-shaped layer
-// with 8-bit moments: 518 us with 8, 534 with 16, 548 with 4).
-int unit_blocks(const sf_dense *t, int n, int sms)
+// Blocks of a unit per warp: what makes one round of four CTAs to an SM of a small call, and at most the kernel's own
+// number. The step of 2^26 x 3.1 elements, with 2, 4, 8 and 16 blocks: fp32 moments and weights 884, 873, 890 and 907 us;
+// 8-bit moments 526, 501, 514 and 528 us over fp32 weights, 457, 394, 352 and 344 us over bf16 ones, where the unit's
+// beginning counts for more. The norm: 117, 76, 71 and 74 us.
+constexpr int kStepBlocks = 4, kCodedBlocks = 8, kNormBlocks = 8;
+
+int unit_blocks(const sf_dense *t, int n, int sms, int most)
 {
     int64_t blocks = 0;
     for (int i = 0; i < n; ++i) blocks += (t[i].n + kBlock - 1) / kBlock;
     const int64_t round = (int64_t)sms * kWarps * 4, each = (blocks + blocks / 8 + round - 1) / round;
-    return each >= 8 ? 8 : each >= 1 ? (int)each : 1;
+    return each >= most ? most : each >= 1 ? (int)each : 1;
 }
 
 // The next launch's tensors, from *at on: those with moments of the given type, or all (-1). Returns the units, or -1
@@ -655,7 +680,7 @@ struct NormArgs {
 template <int N>
 int launch_norm(const sf_dense *t, int n, int sms, const NormArgs &a)
 {
-    const int per = unit_blocks(t, n, sms);
+    const int per = unit_blocks(t, n, sms, kNormBlocks);
     const int64_t cap = (int64_t)sms * kMaxGridPerSm;
     DenseBatch<N> b;
     // the CTAs of all launches, so that the last one of them knows itself
@@ -691,7 +716,8 @@ int launch_step(const sf_dense *t, int n, int per, bool last, StepArgs a, uint32
         const int64_t units = fill(b, t, n, &at, per, state);
         if (units < 0) return SF_ERR_UNSUPPORTED;
         a.last = last && li == launches - 1;
-        // a CTA to a unit: dealt out as SMs come free (8-bit moments: 518 us against 588 with eight CTAs to an SM)
+        // a CTA to a unit: dealt out as SMs come free (a 7B-shaped layer with 8-bit moments, when this was chosen: 518 us
+        // against 588 with eight CTAs to an SM that took units in turn)
         const int rc = launch_early(adamw_kernel<N, CODED>, (int)units, stream, b, a, status);
         if (rc != SF_OK) return rc;
     }
@@ -771,10 +797,9 @@ extern "C" int sf_adamw_step(const sf_dense *t, int n, const sf_adam *hp, int32_
         count_step_kernel<<<1, 1, 0, as_stream(stream)>>>(step, factor, dev_status);
         return launch_status();
     }
-    const int per = unit_blocks(t, n, sms);
     if (full > coded) {
-        rc = launch_steps<false>(t, n, per, coded == 0, a, dev_status, as_stream(stream));
+        rc = launch_steps<false>(t, n, unit_blocks(t, n, sms, kStepBlocks), coded == 0, a, dev_status, as_stream(stream));
         if (rc != SF_OK) return rc;
     }
-    return coded ? launch_steps<true>(t, n, per, true, a, dev_status, as_stream(stream)) : SF_OK;
+    return coded ? launch_steps<true>(t, n, unit_blocks(t, n, sms, kCodedBlocks), true, a, dev_status, as_stream(stream)) : SF_OK;
 }
