@@ -411,7 +411,8 @@ int sf_masked_dw_phase(const sf_dw_problem *probs /* host [n] */, int n, void *w
  * ready for the next. Calls that can overlap need workspaces of their own.
  *
  * Requirements: n >= 0; p, g, m, v, live 16-byte aligned; p fp32 or bf16; g fp32, bf16 or fp16;
- * m_scale, v_scale present for 8-bit moments. Buffers of one call must not overlap.
+ * m_scale, v_scale present for 8-bit moments. Buffers of one call must not overlap, but live may
+ * be a bf16 p itself.
  * Launches: one per 384 non-empty tensors; the step's tensors with fp32 and with 8-bit moments are
  * launched apart. Errors: SF_ERR_ARG, SF_ERR_ALIGN, SF_ERR_UNSUPPORTED (over 2^40 elements).
  */

@@ -495,8 +495,8 @@ def _stream_on(index: int, stream) -> int | None:
 def dense_tensor(p, g, m, v, live=None, decay: float = 1.0, m_scale=None, v_scale=None) -> Desc:
     """One tensor of an AdamW step. p fp32 or bf16; g fp32, bf16 or fp16; m, v fp32, or e4m3 codes
     (float8_e4m3fn or uint8) with one fp32 scale per SF_DENSE_BLOCK elements; live (optional) bf16,
-    written with the stepped weights; decay multiplies the step's weight decay (0: none). All
-    contiguous, of one length."""
+    written with the stepped weights (bf16 weights may be their own); decay multiplies the step's
+    weight decay (0: none). All contiguous, of one length."""
     n = p.numel()
     for t in (p, g, m, v, live):
         if t is not None and (t.numel() != n or not t.is_contiguous()):
@@ -508,6 +508,8 @@ def dense_tensor(p, g, m, v, live=None, decay: float = 1.0, m_scale=None, v_scal
         raise ValueError("m and v must have one type")
     if live is not None and live.dtype not in (torch.bfloat16, torch.int16):
         raise ValueError("live must hold bf16")
+    if live is not None and pt == SF_TYPE_BF16 and live.data_ptr() == p.data_ptr():
+        live = None                                      # bf16 weights are their own live copy
     if st == SF_TYPE_E4M3:
         blocks = -(-n // SF_DENSE_BLOCK)
         for s in (m_scale, v_scale):
@@ -540,8 +542,7 @@ class Dense:
         self.live = p.to(torch.bfloat16) if live else None
 
     def desc(self) -> Desc:
-        live = None if self.live is self.p else self.live            # bf16 weights are their own live copy
-        return dense_tensor(self.p, self.g, self.m, self.v, live, self.decay, self.m_scale, self.v_scale)
+        return dense_tensor(self.p, self.g, self.m, self.v, self.live, self.decay, self.m_scale, self.v_scale)
 
 
 class DenseTensors:

@@ -207,3 +207,13 @@ def test_shared_buffers_are_refused(sf):
     X = normal(16, 16)
     with pytest.raises(RuntimeError, match="sf_grouped_forward"):
         sf.sf_grouped_forward(sf.grouped_problem(X, normal(2, 16, 16), X, offsets([8, 8])))
+
+
+def test_bf16_weights_as_their_own_live_copy(sf):
+    hp, step = sf.AdamParams(lr=1e-2), [sf.step_words() for _ in range(2)]
+    two = [sf.Dense(normal(1003, seed=1), normal(1003, seed=2)) for _ in range(2)]
+    two[0].live = two[0].p
+    two[1].live = two[1].p.clone()
+    for d, st in zip(two, step):
+        sf.sf_adamw_step(sf.DenseTensors([d]), hp, st)
+    assert torch.equal(two[0].p, two[1].p) and torch.equal(two[1].live, two[1].p)
