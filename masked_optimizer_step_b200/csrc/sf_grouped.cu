@@ -260,6 +260,15 @@ __device__ __forceinline__ PUnit pair_unit(const Plan &pl, const GArgs &g, int m
     return x;
 }
 
+// The accumulator of a unit's first half: a unit of one half takes the two in turn, so that its MMAs need not wait for the
+// unit before to be drained.
+__device__ __forceinline__ int accumulator_of(const PUnit &x, int &turn)
+{
+    if (x.n1) return 0;
+    turn ^= 1;
+    return turn ^ 1;
+}
+
 // The tile size for these offsets: the one whose rounds of units, at the mean cost of a unit, end first. A unit's time
 // is about that of its accumulator columns and 128 more, for its weights and its ends (measured, 4 rounds of 4,096-long
 // sums: 154, 204 and 248 us at 256, 384 and 512 tokens), so large tiles win unless they leave the last round empty.
@@ -395,19 +404,20 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         // ------------------------------ MMA issuer ------------------------------
         if (leader) {
             int stage = 0;
-            uint32_t phase = 0, half_phase = 0;   // half_phase: a bit a half, flipped by each use of it
+            uint32_t phase = 0, half_phase = 0;   // half_phase: a bit an accumulator, flipped by each use of it
+            int turn = 0;
             bool ok = true;
             const uint32_t s0 = smem_u32(smem);
             const uint64_t w0 = TRANS ? mnmajor(s0) : kmajor(s0), x0 = kmajor(s0 + P_HALF_BYTES);
             // one half's MMAs of a stage: 16 of K are 32 bytes of a K-major row, or 16 rows of 128 bytes
-            auto half_stage = [&](int h, int st, uint32_t id, bool first, bool last, bool release) {
+            auto half_stage = [&](int h, int acc, int st, uint32_t id, bool first, bool last, bool release) {
                 const uint64_t dw = w0 + (uint64_t)(st * (stage_bytes >> 4));
                 const uint64_t dx = x0 + (uint64_t)(st * (stage_bytes >> 4) + h * (P_HALF_BYTES >> 4));
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < GK / G_UMMA_K; ++k)
-                        mma_bf16_pair(tmem_base + h * PN, dw + k * (TRANS ? 128 : 2), dx + k * 2, id, !first || k != 0);
-                    if (last) mma_commit_pair(&tfull_bar[h], 3);
+                        mma_bf16_pair(tmem_base + acc * PN, dw + k * (TRANS ? 128 : 2), dx + k * 2, id, !first || k != 0);
+                    if (last) mma_commit_pair(&tfull_bar[acc], 3);
                     if (release) mma_commit_pair(&empty_bar[st], 3);
                 }
                 __syncwarp();
@@ -417,7 +427,8 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                 if (u >= total_units) break;
                 const PUnit x = pair_unit(pl, g, most, u);
                 const uint32_t id0 = idesc(g.type, TRANS, false, x.n0, PM), id1 = idesc(g.type, TRANS, false, x.n1, PM);
-                ok = __all_sync(0xffffffffu, mbar_wait(&tempty_bar[0], (half_phase & 1u) ^ 1u, &abort_flag));
+                const int acc = accumulator_of(x, turn);
+                ok = __all_sync(0xffffffffu, mbar_wait(&tempty_bar[acc], (half_phase >> acc & 1u) ^ 1u, &abort_flag));
                 if (!ok) break;
                 // The first stages of a unit run their first half alone, and then their second: that gives the epilogue
                 // the time of T_AHEAD half stages to drain the second half of the unit before.
@@ -429,24 +440,24 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                     ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[st], ph, &abort_flag));
                     if (!ok) break;
                     tc_fence_after();
-                    half_stage(0, st, id0, kb == 0, kb == nk - 1, false);
+                    half_stage(0, 0, st, id0, kb == 0, kb == nk - 1, false);
                 }
                 if (ok && ahead) ok = __all_sync(0xffffffffu, mbar_wait(&tempty_bar[1], (half_phase >> 1) ^ 1u, &abort_flag));
                 if (!ok) break;
                 tc_fence_after();
                 for (kb = 0; kb < ahead; ++kb) {
-                    half_stage(1, stage, id1, kb == 0, kb == nk - 1, true);
+                    half_stage(1, 1, stage, id1, kb == 0, kb == nk - 1, true);
                     if (++stage == stages) { stage = 0; phase ^= 1u; }
                 }
                 for (; kb < nk; ++kb) {
                     ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, &abort_flag));
                     if (!ok) break;
                     tc_fence_after();
-                    half_stage(0, stage, id0, kb == 0, kb == nk - 1, x.n1 == 0);
-                    if (x.n1) half_stage(1, stage, id1, false, kb == nk - 1, true);
+                    half_stage(0, acc, stage, id0, kb == 0, kb == nk - 1, x.n1 == 0);
+                    if (x.n1) half_stage(1, 1, stage, id1, false, kb == nk - 1, true);
                     if (++stage == stages) { stage = 0; phase ^= 1u; }
                 }
-                half_phase ^= x.n1 ? 3u : 1u;
+                half_phase ^= x.n1 ? 3u : 1u << acc;
             }
             if (elect_one()) mma_commit_pair(&drain_bar, 3);
             __syncwarp();
@@ -456,23 +467,26 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
     } else {
         // --------------------------- epilogue (warps 2..9) ---------------------------
         const int quad = warp & 3;              // TMEM lanes 32*quad .. 32*quad+31
-        const int part = (warp - 2) >> 2;       // 128 of a half's columns
+        const int part = (warp - 2) >> 2;       // each has half of a half's columns
         uint8_t *s_out = smem + T_RING_BYTES + part * T_OUT_BYTES;
         uint32_t half_phase = 0;
+        int turn = 0;
         bool ready = true;
         for (int i = 0; i * workers < total_units && ready; ++i) {
             const int u = unit_of(i, worker, workers);
             if (u >= total_units) break;
             const PUnit x = pair_unit(pl, g, most, u);
             const int m = x.m0 + (int)crank * 128, bytes = 2 * min(128, g.M - m);
+            const int first = accumulator_of(x, turn);
             for (int h = 0; h < (x.n1 ? 2 : 1); ++h) {
-                ready = mbar_wait(&tfull_bar[h], half_phase >> h & 1u, &abort_flag);
+                const int acc = h + first;
+                ready = mbar_wait(&tfull_bar[acc], half_phase >> acc & 1u, &abort_flag);
                 ready = bar_all(1 + part, 128, ready);       // the part's warps go on together or not at all
                 if (!ready) break;
                 tc_fence_after();
                 // all of this warp's columns, packed, into registers, so that the MMAs get the accumulator back at once
-                const int c0 = part * 128, cols = (h ? x.n1 : x.n0) - c0;
-                const uint32_t t_row = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(h * PN + c0);
+                const int n = h ? x.n1 : x.n0, c0 = part * ((n / 2 + 31) & ~31), cols = part ? n - c0 : min(n, (n / 2 + 31) & ~31);
+                const uint32_t t_row = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * PN + c0);
                 uint32_t w[4][16];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -487,8 +501,8 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (leader) mbar_arrive(&tempty_bar[h]);
-                    else mbar_arrive_remote(&tempty_bar[h], 0);
+                    if (leader) mbar_arrive(&tempty_bar[acc]);
+                    else mbar_arrive_remote(&tempty_bar[acc], 0);
                 }
                 // Out through shared memory, 32 tokens at a time: the part's four warps lay down each token's 128
                 // features, 64 bytes a warp, and a lane sends each token's row as one bulk copy.
@@ -512,7 +526,7 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                     bulk_commit();
                 }
             }
-            half_phase ^= x.n1 ? 3u : 1u;
+            half_phase ^= x.n1 ? 3u : 1u << first;
         }
         bulk_wait_all();
     }
@@ -1656,10 +1670,10 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
     // 32.1 us); long ones come out more even as a CTA each (the decode batch above: 114.6 against 117.5 us).
     const bool rounds = s == 1 && tiles * m_tiles > 2 * sms && nk <= 24;
     const int stage_bytes = S_W_BYTES + s * nb * GK * 2;
-    g.stages = 100 * 1024 / stage_bytes;
-    if (g.stages > S_MAX_STAGES) g.stages = S_MAX_STAGES;
     const int rows = SM_ROWS / s;
     const int64_t units = tiles * ((g.M + rows - 1) / rows);                       // at most
+    g.stages = (units <= sms ? 200 : 100) * 1024 / stage_bytes;                    // one CTA to an SM, or two
+    if (g.stages > S_MAX_STAGES) g.stages = S_MAX_STAGES;
     const int box_rows = fwd ? rows : 64, box_bytes = !fwd && s == 4 ? 64 : 128;
     if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, box_rows, box_bytes) ||
         !encode(&g.tm_x, p->type, x, g.K, p->T, ld_x, 0, 0, nb))
