@@ -459,8 +459,8 @@ int sf_adamw_step(const sf_dense *t /* host [n] */, int n, const sf_adam *hp, in
  * results whose sums hold it.
  * offsets must not fall and must lie in [0, T]: otherwise nothing is computed and SF_STATUS_BAD_OFFSET is
  * set. Pipeline waits are bounded as in sf_masked_dw (SF_STATUS_WAIT_TIMEOUT).
- * Deterministic: every result is summed by one CTA or pair of CTAs in an order that the sizes and, for the
- * weight gradient, the expert's tokens give; which rows share a tile changes no sum. The written operand
+ * Deterministic: every result is summed in an order that the sizes and, for the weight gradient, the
+ * expert's tokens give; which rows share a tile changes no sum. The written operand
  * must not overlap the others (one address for two operands is refused). Requirements: 1 <= E <= 1024; T >= 0; R, C positive multiples of 8;
  * ld_a >= C, ld_y >= R, ld_w >= C, stride_w >= (R - 1) * ld_w + C when E > 1; strides multiples of 8 elements
  * (4 for an fp32 W); A, W, Y 16-byte aligned (A and Y may be NULL when T = 0). One launch a call.

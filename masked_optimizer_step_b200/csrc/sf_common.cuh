@@ -205,6 +205,18 @@ SF_DEVICE void tma_load_2d(void *dst, const CUtensorMap *m, uint64_t *bar, int x
         : "memory");
 }
 
+// Two floats of the shared memory of CTA `rank` of the cluster, at the place that `addr` is in this CTA's.
+SF_DEVICE float2 ld_cluster_f32x2(uint32_t addr, int rank)
+{
+    float2 v;
+    asm volatile(
+        "{\n\t.reg .b32 ra;\n\t"
+        "mapa.shared::cluster.u32 ra, %2, %3;\n\t"
+        "ld.shared::cluster.v2.f32 {%0, %1}, [ra];\n\t}"
+        : "=f"(v.x), "=f"(v.y) : "r"(addr), "r"(rank) : "memory");
+    return v;
+}
+
 // 2-D tiled TMA load by either CTA of a pair into its own shared memory, completing its bytes on
 // the mbarrier at `bar`'s offset in the even CTA (the one whose thread issues the pair's MMAs).
 // No multicast.

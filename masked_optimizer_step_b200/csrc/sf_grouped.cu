@@ -78,6 +78,7 @@ struct GArgs {
     int64_t ld_out, stride_out;
     int32_t E, T, M, K, type;  // M: accumulator rows in all (forward R, dx C, dw R); K: forward C, dx R, dw C (its N)
     int32_t nb, stages;              // single CTAs: token box, stages
+    int32_t split;                   // forward, dx in slices: CTAs (a cluster) that share a unit's K
     int32_t out_f32, accumulate;     // dw
 };
 
@@ -550,8 +551,10 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 // 128 / S accumulator rows and S slices of K: the M operand holds the same weight rows S times, slice j of K in rows
 // j * 128 / S .., the N operand the tokens S times, slice j in columns j * nb ... The products of one slice with itself
 // are the partial sums wanted; those of different slices are not read. S times the units, a S-th of the steps, and no
-// exchange between CTAs. (Splitting K over the CTAs of a cluster, which exchange partial sums through distributed shared
-// memory, took 63 us where one slice took 27: 16 experts, 777 tokens, 2056 x 1416.)
+// exchange between CTAs. Where that still leaves most SMs without work, the slices of a unit lie in the CTAs of a cluster,
+// S in each; every CTA adds up its own and then, out of the others' shared memory, its share of the unit's results. (In
+// clusters alone, without the slices, a call with more units took 63 us where one slice took 27: 16 experts, 777 tokens,
+// 2056 x 1416.)
 // ------------------------------------------------------------------------------------------------
 
 struct SUnit {
@@ -647,12 +650,14 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         order_experts(pl, g.E, [](int cnt) { return cnt; });
         count_units(pl, g.E, [&](int cnt) { return cnt > 0 ? quot_up(cnt, tile_tokens(cnt, nb, 16)) * m_tiles : 0; });
     }
-    const int nk = ((g.K + GK - 1) / GK + S - 1) / S;          // steps of each slice (the last slice's may lie behind K: zeros)
+    const int split = S > 1 ? g.split : 1, rank = S > 1 && split > 1 ? (int)cluster_ctarank() : 0;
+    // steps of each slice (the last slices' may lie behind K: zeros)
+    const int nk = ((g.K + GK - 1) / GK + S * split - 1) / (S * split);
     const int stage_bytes = S_W_BYTES + S * nb * GK * 2;
     // this CTA's i-th unit
     SUnit only;
     only.n = 0;
-    if (!ROUNDS && valid) only = scan_unit(pl.off, g.E, nb, blockIdx.x, m_tiles);
+    if (!ROUNDS && valid) only = scan_unit(pl.off, g.E, nb, split > 1 ? blockIdx.x / split : blockIdx.x, m_tiles);
     auto unit = [&](int i) {
         SUnit x;
         x.n = 0;
@@ -677,7 +682,7 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                     mbar_arrive_expect_tx(&full_bar[stage], stage_bytes);
 #pragma unroll
                     for (int j = 0; j < S; ++j) {
-                        const int k = (j * nk + i) * GK;
+                        const int k = ((rank * S + j) * nk + i) * GK;
                         if (TRANS && S == 1) {
                             tma_load_3d(sw, &g.tm_w, &full_bar[stage], m0, k, x.e);
                             tma_load_3d(sw + G_BOX_BYTES, &g.tm_w, &full_bar[stage], m0 + 64, k, x.e);
@@ -791,7 +796,9 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                         s.x = __fadd_rn(s.x, a.x);
                         s.y = __fadd_rn(s.y, a.y);
                     }
-                    if (m0 + row < g.M)
+                    if (split > 1)              // to be added up with the other CTAs'
+                        *reinterpret_cast<float2 *>(part + t * ROWS + row) = s;
+                    else if (m0 + row < g.M)
                         *reinterpret_cast<uint32_t *>(out + (int64_t)t * g.ld_out + m0 + row) =
                             pack2(__float_as_uint(s.x), __float_as_uint(s.y), g.type);
                 }
@@ -801,6 +808,24 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (S > 1 && split > 1) {                  // the CTAs' sums, in their order; each CTA has a share of the unit's results
+        cluster_sync();
+        const uint32_t part = smem_u32(smem);
+        for (int i = rank * S_THREADS + tid; i < only.n * (ROWS / 2); i += split * S_THREADS) {
+            const int t = i / (ROWS / 2), row = 2 * (i - t * (ROWS / 2)), m0 = only.mt * ROWS;
+            float2 s = make_float2(0.0f, 0.0f);
+            for (int c = 0; c < split; ++c) {
+                const float2 a = ld_cluster_f32x2(part + (t * ROWS + row) * 4, c);
+                s.x = __fadd_rn(s.x, a.x);
+                s.y = __fadd_rn(s.y, a.y);
+            }
+            if (m0 + row < g.M)
+                *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(g.out) + (int64_t)(only.t0 + t) * g.ld_out + m0 + row) =
+                    pack2(__float_as_uint(s.x), __float_as_uint(s.y), g.type);
+        }
+        __syncwarp();
+        cluster_sync();                         // no CTA leaves while others read its sums
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, (uint32_t)tmem_cols);
@@ -1672,7 +1697,14 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
     const int stage_bytes = S_W_BYTES + s * nb * GK * 2;
     const int rows = SM_ROWS / s;
     const int64_t units = tiles * ((g.M + rows - 1) / rows);                       // at most
-    g.stages = (units <= sms ? 200 : 100) * 1024 / stage_bytes;                    // one CTA to an SM, or two
+    // The slices over the CTAs of a cluster, too, while the units still fit and a CTA keeps two steps or more (alone against
+    // in clusters: one expert of 64 x 4096 over 16 tokens 10.7 / 5.0 us, 512 x 11008 over 100 tokens 45.3 / 11.4, 4096 x 4096
+    // over 2 tokens 11.0 / 8.9; with a step a CTA, 2 experts of 512 x 512 over 2 tokens each, 4.0 / 4.7).
+    g.split = 1;
+    while (s > 1 && g.split < 8 && units * 2 * g.split <= 2 * sms && nk >= 2 * 2 * g.split * s) g.split *= 2;
+    // One CTA to an SM, or two. Clusters do not fill every SM (8 experts of 128 x 2048 over 2 tokens each, 144 CTAs in
+    // clusters of 4: 7.9 us with one to an SM, 5.3 with two).
+    g.stages = (units * g.split <= (g.split > 1 ? sms * 3 / 4 : sms) ? 200 : 100) * 1024 / stage_bytes;
     if (g.stages > S_MAX_STAGES) g.stages = S_MAX_STAGES;
     const int box_rows = fwd ? rows : 64, box_bytes = !fwd && s == 4 ? 64 : 128;
     if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, box_rows, box_bytes) ||
@@ -1680,8 +1712,8 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
         return SF_ERR_CUDA;
     auto kernel = rounds ? grouped_small_kernel<TRANS, 1, true> : s == 1 ? grouped_small_kernel<TRANS, 1, false>
                   : s == 2 ? grouped_small_kernel<TRANS, 2, false> : grouped_small_kernel<TRANS, 4, false>;
-    const int grid = (int)(rounds ? 2 * sms : units);
-    return launch(kernel, grid, 1, S_THREADS, (size_t)g.stages * stage_bytes + 1024, g, status, stream);
+    const int grid = (int)(rounds ? 2 * sms : units * g.split);
+    return launch(kernel, grid, g.split, S_THREADS, (size_t)g.stages * stage_bytes + 1024, g, status, stream);
 }
 
 }  // namespace

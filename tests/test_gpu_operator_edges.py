@@ -117,6 +117,24 @@ def test_tiles_of_every_width(sf, counts, dt):
     assert int(status) == 0
 
 
+@pytest.mark.parametrize("counts,M,K", [([1], 64, 4096), ([16], 72, 4104), ([42], 248, 7912), ([100], 520, 11008), ([3, 0, 9, 4], 64, 4096),
+                                        ([2, 2], 1032, 4096), ([100, 0, 90], 264, 2568), ([2], 4096, 4096), ([0, 1, 0], 8, 8200),
+                                        ([10, 22, 1, 0, 30, 64, 17, 8], 64, 2056), ([17] * 32, 64, 2048)])
+@pytest.mark.parametrize("dt", [BF, torch.float16])
+def test_few_rows_and_long_sums(sf, counts, M, K, dt):
+    """Few results over a long K, whose slices are spread over SMs."""
+    off, T, E, status = offsets(counts), sum(counts), len(counts), sf.status_word()
+    A, W, Y = normal(T, K, dt=dt, seed=10), normal(E, M, K, dt=dt, seed=11), torch.full((T + 2, M), 7.0, dtype=dt, device=DEV)
+    sf.sf_grouped_forward(sf.grouped_problem(A, W, Y[:T], off), status)
+    dY, Wt, dA = normal(T, K, dt=dt, seed=12), normal(E, K, M, dt=dt, seed=13), torch.full((T + 2, M), 7.0, dtype=dt, device=DEV)
+    sf.sf_grouped_dx(sf.grouped_problem(dA[:T], Wt, dY, off), status)
+    for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+        if a < b:
+            check(Y[a:b], A[a:b].double(), W[e].double().t())
+            check(dA[a:b], dY[a:b].double(), Wt[e].double())
+    assert bool((Y[T:] == 7).all()) and bool((dA[T:] == 7).all()) and int(status) == 0
+
+
 def chain(sf, T=700, E=5, R=520, C=264, seed=0):
     """Forward, gradients, norm and step of one expert projection: every call reads what the one before wrote."""
     W, A, dY = normal(E, R, C, dt=F32, seed=seed) * 0.05, normal(T, C, seed=seed + 1), normal(T, R, seed=seed + 2) * 0.01
