@@ -78,7 +78,7 @@ struct GArgs {
     int64_t ld_out, stride_out;
     int32_t E, T, M, K, type;  // M: accumulator rows in all (forward R, dx C, dw R); K: forward C, dx R, dw C (its N)
     int32_t nb, stages;              // single CTAs: token box, stages
-    int32_t split;                   // forward, dx in slices: CTAs (a cluster) that share a unit's K
+    int32_t split;                   // single CTAs in slices: CTAs (a cluster) that share a unit's K
     int32_t out_f32, accumulate;     // dw
 };
 
@@ -1241,10 +1241,27 @@ __device__ __forceinline__ void add_box(const uint4 *box, float *dst, int64_t ld
     }
 }
 
+// Four neighbouring sums into W, or added to what it holds.
+__device__ __forceinline__ void put_weights(const GArgs &g, float *w32, uint16_t *w16, int r, int c, float4 s, bool add)
+{
+    if (g.out_f32) {
+        float4 *dst = reinterpret_cast<float4 *>(w32 + r * g.ld_out + c);
+        if (add) {
+            const float4 o = *dst;
+            s = make_float4(__fadd_rn(o.x, s.x), __fadd_rn(o.y, s.y), __fadd_rn(o.z, s.z), __fadd_rn(o.w, s.w));
+        }
+        *dst = s;
+    } else {
+        *reinterpret_cast<uint2 *>(w16 + r * g.ld_out + c) =
+            make_uint2(pack2(__float_as_uint(s.x), __float_as_uint(s.y), g.type), pack2(__float_as_uint(s.z), __float_as_uint(s.w), g.type));
+    }
+}
+
 // A unit is 128 / S rows x 256 / S columns of one expert's W and all its tokens, in S slices of tokens as in the small
 // forward kernel: slice j in rows j * 128 / S .. of the M operand and columns j * 256 / S .. of the N operand, of whose
-// products the S blocks on the diagonal are wanted. While one CTA of an SM waits for its tokens the other writes.
-template <int S>
+// products the S blocks on the diagonal are wanted. While one CTA of an SM waits for its tokens the other writes. As there,
+// the slices of few units lie in the CTAs of a cluster, S in each (SPLIT).
+template <int S, bool SPLIT>
 __global__ void __launch_bounds__(D_THREADS, 2)
 grouped_dw_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 {
@@ -1283,7 +1300,9 @@ grouped_dw_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
     const uint32_t tmem_base = tmem_base_s;
 
     const int n_tiles = (g.K + COLS - 1) / COLS, per = (g.M + ROWS - 1) / ROWS * n_tiles;
-    const int e = quot(blockIdx.x, per), local = blockIdx.x - e * per, mt = quot(local, n_tiles);
+    const int split = SPLIT ? g.split : 1, rank = SPLIT ? (int)cluster_ctarank() : 0;
+    const int u = SPLIT ? blockIdx.x / split : blockIdx.x;
+    const int e = quot(u, per), local = u - e * per, mt = quot(local, n_tiles);
     const int r0 = mt * ROWS, c0 = (local - mt * n_tiles) * COLS;
     const int t0 = bad ? 0 : __ldg(g.offsets + e), cnt = bad ? 0 : __ldg(g.offsets + e + 1) - t0;
     const int rows = min(ROWS, g.M - r0), cols = min(COLS, g.K - c0);
@@ -1295,7 +1314,7 @@ grouped_dw_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
             if (blockIdx.x == 0 && tid == 0) set_status(status, SF_STATUS_BAD_OFFSET);
         } else if (!g.accumulate) {             // an expert without tokens: zeros, 16 bytes to a thread
             const int unit = g.out_f32 ? 4 : 8, line = cols / unit;
-            for (int i = tid; i < rows * line; i += D_THREADS) {
+            for (int i = rank * D_THREADS + tid; i < rows * line; i += split * D_THREADS) {
                 const int r = quot(i, line), c = (i - r * line) * unit;
                 if (g.out_f32) *reinterpret_cast<uint4 *>(w32 + r * g.ld_out + c) = make_uint4(0u, 0u, 0u, 0u);
                 else *reinterpret_cast<uint4 *>(w16 + r * g.ld_out + c) = make_uint4(0u, 0u, 0u, 0u);
@@ -1306,14 +1325,15 @@ grouped_dw_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         return;
     }
     if (g.accumulate)                           // what W holds, on its way while the MMAs run
-        for (int i = tid; i < rows * (COLS / 32); i += D_THREADS) {
+        for (int i = rank * D_THREADS + tid; i < rows * (COLS / 32); i += split * D_THREADS) {
             const int r = i / (COLS / 32), c = (i - r * (COLS / 32)) * 32;
             if (c < cols) prefetch_l2(w32 + r * g.ld_out + c);
         }
-    const int nk = ((cnt + GK - 1) / GK + S - 1) / S;          // steps of each slice
+    const int nk = ((cnt + GK - 1) / GK + S * split - 1) / (S * split);      // steps of each slice
     const int chunks = g.out_f32 ? quot_up(nk, W_CHUNK_STAGES) : 1, chunk = quot_up(nk, chunks);
     // slice j's tokens in its step i, those of the slice's end and of the expert's end left out
-    auto tokens_of = [&](int j, int i) { return min(GK, cnt - (j * nk + i) * GK); };
+    const int step0 = rank * S * nk;            // of the slices before this CTA's
+    auto tokens_of = [&](int j, int i) { return min(GK, cnt - (step0 + j * nk + i) * GK); };
     int stage = 0, sent = 0;
     uint32_t phase = 0;
     for (int ch = 0; ch < chunks; ++ch) {
@@ -1327,7 +1347,7 @@ grouped_dw_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 #pragma unroll
                     for (int j = 0; j < S; ++j) {
                         // a step behind the end reads behind the last row: zeros
-                        const int t = tokens_of(j, i) > 0 ? t0 + (j * nk + i) * GK : g.T;
+                        const int t = tokens_of(j, i) > 0 ? t0 + (step0 + j * nk + i) * GK : g.T;
                         tma_load_2d(sy + j * (P_HALF_BYTES / S), &g.tm_x, &full_bar[stage], r0, t);
                         if (S == 1) tma_load_2d(sy + G_BOX_BYTES, &g.tm_x, &full_bar[stage], r0 + 64, t);
 #pragma unroll
@@ -1387,10 +1407,10 @@ grouped_dw_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         __syncwarp();
         if (!mbar_wait(&done_bar, (uint32_t)(ch & 1), &abort_flag)) abort_flag = 1;
         __syncthreads();
-        if (abort_flag) break;
+        if (abort_flag && !SPLIT) break;    // the CTAs of a cluster go on together
         tc_fence_after();
         const bool add = g.accumulate || ch > 0;
-        if (warp >= 2) {
+        if (warp >= 2 && !(SPLIT && abort_flag)) {
             const int quad = warp & 3, part = (warp - 2) >> 2;
             const int slice = quad * S / 4;
             // this warp's 32 accumulator rows and its half of the slice's columns
@@ -1466,20 +1486,28 @@ grouped_dw_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                         const float4 a = *reinterpret_cast<const float4 *>(part_sums + (j * ROWS + r) * PITCH + c);
                         s = make_float4(__fadd_rn(s.x, a.x), __fadd_rn(s.y, a.y), __fadd_rn(s.z, a.z), __fadd_rn(s.w, a.w));
                     }
-                    if (g.out_f32) {
-                        float4 *dst = reinterpret_cast<float4 *>(w32 + r * g.ld_out + c);
-                        if (add) {
-                            const float4 o = *dst;
-                            s = make_float4(__fadd_rn(o.x, s.x), __fadd_rn(o.y, s.y), __fadd_rn(o.z, s.z), __fadd_rn(o.w, s.w));
-                        }
-                        *dst = s;
-                    } else {
-                        *reinterpret_cast<uint2 *>(w16 + r * g.ld_out + c) =
-                            make_uint2(pack2(__float_as_uint(s.x), __float_as_uint(s.y), g.type),
-                                       pack2(__float_as_uint(s.z), __float_as_uint(s.w), g.type));
-                    }
+                    if (SPLIT) *reinterpret_cast<float4 *>(part_sums + r * PITCH + c) = s;    // to be added to the other CTAs'
+                    else put_weights(g, w32, w16, r, c, s, add);
                 }
             }
+        }
+        if (SPLIT) {                            // the CTAs' sums, in their order; each CTA has a share of the unit's results
+            __syncwarp();
+            cluster_sync();
+            const uint32_t part_sums = smem_u32(smem);
+            for (int i = rank * D_THREADS + tid; i < ROWS * (COLS / 4); i += split * D_THREADS) {
+                const int r = i / (COLS / 4), c = (i - r * (COLS / 4)) * 4;
+                if (r >= rows || c >= cols || abort_flag) continue;
+                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int o = 0; o < split; ++o) {
+                    const uint32_t from = part_sums + (r * PITCH + c) * 4;
+                    const float2 a = ld_cluster_f32x2(from, o), b = ld_cluster_f32x2(from + 8, o);
+                    s = make_float4(__fadd_rn(s.x, a.x), __fadd_rn(s.y, a.y), __fadd_rn(s.z, b.x), __fadd_rn(s.w, b.y));
+                }
+                put_weights(g, w32, w16, r, c, s, add);
+            }
+            __syncwarp();
+            cluster_sync();                     // no CTA goes on while others read its sums
         }
         tc_fence_before();
         if (ch + 1 < chunks) fence_proxy_async_smem();            // the stages go back to TMA
@@ -1701,7 +1729,7 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
     // in clusters: one expert of 64 x 4096 over 16 tokens 10.7 / 5.0 us, 512 x 11008 over 100 tokens 45.3 / 11.4, 4096 x 4096
     // over 2 tokens 11.0 / 8.9; with a step a CTA, 2 experts of 512 x 512 over 2 tokens each, 4.0 / 4.7).
     g.split = 1;
-    while (s > 1 && g.split < 8 && units * 2 * g.split <= 2 * sms && nk >= 2 * 2 * g.split * s) g.split *= 2;
+    while (s > 1 && g.split < 8 && units * 2 * g.split <= sms * 7 / 4 && nk >= 2 * 2 * g.split * s) g.split *= 2;
     // One CTA to an SM, or two. Clusters do not fill every SM (8 experts of 128 x 2048 over 2 tokens each, 144 CTAs in
     // clusters of 4: 7.9 us with one to an SM, 5.3 with two).
     g.stages = (units * g.split <= (g.split > 1 ? sms * 3 / 4 : sms) ? 200 : 100) * 1024 / stage_bytes;
@@ -1777,11 +1805,17 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
     // 24 us with 1, 2 and 4 slices; where they do not fit, every slice more costs its share of the loads again).
     int s = 1;
     while (s < 4 && busy * tiles(SM_ROWS / (2 * s), PN / (2 * s)) <= 2 * sms && p->T > (int64_t)GK * s * p->E) s *= 2;
+    g.split = 1;
+    // Four slices in each CTA of a cluster while the CTAs fit one to an SM and keep more than four steps (alone against in
+    // clusters: one expert of 128 x 128 over 65,536 tokens 151 / 31 us, of 64 x 512 over 8,192 tokens 22.3 / 9.5; with
+    // shorter sums or fewer slices clusters cost what they save).
     const int64_t units = p->E * tiles(SM_ROWS / s, PN / s);
-    g.stages = units <= sms ? 4 : 2;                     // one CTA to an SM, or two
+    while (s == 4 && g.split < 8 && units * 2 * g.split <= sms && p->T > (int64_t)4 * GK * 4 * 2 * g.split * p->E) g.split *= 2;
+    g.stages = units * g.split <= (g.split > 1 ? sms * 3 / 4 : sms) ? 4 : 2;       // one CTA to an SM, or two
     if (!encode(&g.tm_w, p->type, a, p->C, p->T, ld_a, 0, 0, 64) ||
         !encode(&g.tm_x, p->type, y, p->R, p->T, ld_y, 0, 0, 64, s == 4 ? 64 : 128))
         return SF_ERR_CUDA;
-    auto kernel = s == 1 ? grouped_dw_small_kernel<1> : s == 2 ? grouped_dw_small_kernel<2> : grouped_dw_small_kernel<4>;
-    return launch(kernel, (int)units, 1, D_THREADS, (size_t)g.stages * D_STAGE_BYTES + 1024, g, dev_status, stream);
+    auto kernel = g.split > 1 ? grouped_dw_small_kernel<4, true> : s == 1 ? grouped_dw_small_kernel<1, false>
+                  : s == 2 ? grouped_dw_small_kernel<2, false> : grouped_dw_small_kernel<4, false>;
+    return launch(kernel, (int)units * g.split, g.split, D_THREADS, (size_t)g.stages * D_STAGE_BYTES + 1024, g, dev_status, stream);
 }

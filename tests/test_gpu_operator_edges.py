@@ -135,6 +135,24 @@ def test_few_rows_and_long_sums(sf, counts, M, K, dt):
     assert bool((Y[T:] == 7).all()) and bool((dA[T:] == 7).all()) and int(status) == 0
 
 
+@pytest.mark.parametrize("counts,R,C", [([8192], 64, 512), ([65001], 128, 128), ([9000, 0, 3], 72, 136), ([5, 20011], 8, 264), ([0, 4500], 64, 64)])
+@pytest.mark.parametrize("out,add", [(F32, False), (F32, True), (BF, False)])
+def test_few_weights_and_many_tokens(sf, counts, R, C, out, add):
+    """Small weight gradients over many tokens, whose slices are spread over SMs."""
+    off, T, E, status = offsets(counts), sum(counts), len(counts), sf.status_word()
+    A, Y, G = normal(T, C, seed=14), normal(T, R, seed=15), normal(E, R, C, dt=out, seed=16)
+    before = G.double() if add else torch.zeros_like(G, dtype=torch.float64)
+    sf.sf_grouped_dw(sf.grouped_problem(A, G, Y, off), status, accumulate=add)
+    for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+        y, x = Y[a:b].double(), A[a:b].double()
+        ref, size = y.t() @ x + before[e], y.abs().t() @ x.abs() + before[e].abs()
+        slack = ((b - a) / 16 + 32) * 2.0 ** -23 * size
+        assert bool(((G[e].double() - ref).abs() <= slack + torch.finfo(out).eps / 2 * (ref.abs() + slack)).all())
+        if out == F32 and not add and b - a > 4000:        # far from the bound: chunks keep sums of any length this near
+            assert float((G[e].double() - ref).norm()) < 1e-6 * float(ref.norm())
+    assert int(status) == 0
+
+
 def chain(sf, T=700, E=5, R=520, C=264, seed=0):
     """Forward, gradients, norm and step of one expert projection: every call reads what the one before wrote."""
     W, A, dY = normal(E, R, C, dt=F32, seed=seed) * 0.05, normal(T, C, seed=seed + 1), normal(T, R, seed=seed + 2) * 0.01
