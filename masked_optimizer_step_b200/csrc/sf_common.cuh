@@ -395,6 +395,12 @@ SF_DEVICE void bulk_store(void *dst, const void *src, uint32_t bytes)
 }
 
 // 3-D tiled TMA store of a box {x, y, z} from shared memory, or its addition (fp32) to what is there.
+SF_DEVICE void tma_store_2d(const CUtensorMap *m, const void *src, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
+                 ::"l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_u32(src)) : "memory");
+}
+
 SF_DEVICE void tma_store_3d(const CUtensorMap *m, const void *src, int x, int y, int z)
 {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];"
