@@ -71,8 +71,11 @@ __device__ __forceinline__ int cand_tokens(int i) { return T_TOKENS - 32 * i; } 
 
 struct GArgs {
     CUtensorMap tm_w;          // forward, dx: W as {C, R, E}; dw: A as {C, T}
-    CUtensorMap tm_x;          // tokens: forward A, dx Y as {K, T}; dw: Y as {R, T}
-    CUtensorMap tm_out;        // dw: W as {C, R, E}, boxes of 128 bytes x 32 rows; CTA pairs: tm_x with boxes half as high
+    CUtensorMap tm_x;          // dw: Y as {R, T}
+    CUtensorMap tm_out;        // dw: W as {C, R, E}, boxes of 128 bytes x 32 rows
+    // forward, dx: tokens, A or Y as {K, T}, in boxes of as many rows as a tile needs (a box more costs more than its
+    // rows): 32, 64, 96 and 128 for CTA pairs, 16, 32, 64 and 128 for single CTAs
+    CUtensorMap tm_t[4];
     CUtensorMap tm_y;          // CTA pairs: the output as {M, T}, boxes of 128 features x 16 tokens
     const int32_t *offsets;
     void *out;
@@ -330,8 +333,7 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
         mbar_init(&drain_bar, 1);
         fence_mbarrier_init();
         prefetch_tmap(&g.tm_w);
-        prefetch_tmap(&g.tm_x);
-        prefetch_tmap(&g.tm_out);
+        for (int b = 0; b < 4; ++b) prefetch_tmap(&g.tm_t[b]);
         prefetch_tmap(&g.tm_y);
     }
     griddep_wait();                             // what the launches before this one wrote is there from here on
@@ -342,8 +344,9 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
     const int most = choose_tile(pl, g, workers);
     // The ring's stages hold what the tiles need: 8 of 24 KB, 6 of 32 KB or 4 of 48 KB. Tiles of up to 128 tokens are
     // bound by the requests to L2 (boxes asked for into L2 ahead of their loads cost 5 to 20% more time), so their token
-    // boxes are half as high: 16 experts of 2048 x 2048 over 2048 tokens 39.0 -> 35.7 us, 48 of 1416 x 2056 over 5000
-    // 77.6 -> 69.5 us, with an expert of half the tokens among them 90.7 -> 78.3 us.
+    // boxes are as high as they need (half as high, when this was measured: 16 experts of 2048 x 2048 over 2048 tokens
+    // 39.0 -> 35.7 us, 48 of 1416 x 2056 over 5000 77.6 -> 69.5 us, with an expert of half the tokens among them
+    // 90.7 -> 78.3 us).
     const int stages = most <= 128 ? 8 : most <= PN ? 6 : 4, stage_bytes = T_RING_BYTES / stages;
     order_experts(pl, g.E, [&](int cnt) { return cnt > 0 ? tile_tokens(cnt, most, 32) : 0; });
     count_units(pl, g.E, [&](int cnt) { return cnt > 0 ? quot_up(cnt, tile_tokens(cnt, most, 32)) * ((g.M + PM - 1) / PM) : 0; });
@@ -370,9 +373,9 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                 const PUnit x = pair_unit(pl, g, most, u);
                 const int m = x.m0 + (int)crank * 128;
                 const int ta = x.t0 + (int)crank * (x.n0 / 2), tb = x.t0 + x.n0 + (int)crank * (x.n1 / 2);
-                const bool low = x.n0 <= 128;         // 64 rows of tokens to a CTA at most: the low box
-                const CUtensorMap *tx = low ? &g.tm_out : &g.tm_x;
-                const uint32_t bytes = (uint32_t)P_HALF_BYTES * (low ? 3 : x.n1 ? 6 : 4);
+                // this CTA's half of a half's tokens, in quarters of 32 rows
+                const int rows0 = (x.n0 / 2 + 31) / 32, rows1 = (x.n1 / 2 + 31) / 32;
+                const uint32_t bytes = 2 * ((uint32_t)P_HALF_BYTES + (rows0 + rows1) * (P_HALF_BYTES / 4));
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag)) { ok = false; break; }
                     uint8_t *sw = smem + stage * stage_bytes, *sx = sw + P_HALF_BYTES;
@@ -383,8 +386,8 @@ grouped_pair_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                     } else {
                         tma_load_3d_pair(sw, &g.tm_w, &full_bar[stage], kb * GK, m, x.e);
                     }
-                    tma_load_2d_pair(sx, tx, &full_bar[stage], kb * GK, ta);
-                    if (x.n1) tma_load_2d_pair(sx + P_HALF_BYTES, &g.tm_x, &full_bar[stage], kb * GK, tb);
+                    tma_load_2d_pair(sx, &g.tm_t[rows0 - 1], &full_bar[stage], kb * GK, ta);
+                    if (x.n1) tma_load_2d_pair(sx + P_HALF_BYTES, &g.tm_t[rows1 - 1], &full_bar[stage], kb * GK, tb);
                     issued |= 1u << stage;
                     issued_parity = (issued_parity & ~(1u << stage)) | phase << stage;
                     if (++stage == stages) { stage = 0; phase ^= 1u; }
@@ -635,7 +638,7 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&g.tm_w);
-        prefetch_tmap(&g.tm_x);
+        for (int b = 0; 16 << b <= g.nb; ++b) prefetch_tmap(&g.tm_t[b]);
         abort_flag = 0;
         for (int s = 0; s < stages; ++s) {
             mbar_init(&full_bar[s], 1);
@@ -684,11 +687,12 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
             const SUnit x = unit(r);
             if (x.n == 0) break;
             if (lane == 0) {
-                const int m0 = x.mt * ROWS;
+                const int m0 = x.mt * ROWS, high = x.n <= 16 ? 0 : x.n <= 32 ? 1 : x.n <= 64 ? 2 : 3;       // its token box
+                const uint32_t bytes = S_W_BYTES + S * (16 << high) * GK * 2;
                 for (int i = 0; i < nk; ++i) {
                     if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag)) { ok = false; break; }
                     uint8_t *sw = smem + stage * stage_bytes, *sx = sw + S_W_BYTES;
-                    mbar_arrive_expect_tx(&full_bar[stage], stage_bytes);
+                    mbar_arrive_expect_tx(&full_bar[stage], bytes);
 #pragma unroll
                     for (int j = 0; j < S; ++j) {
                         const int k = ((rank * S + j) * nk + i) * GK;
@@ -700,7 +704,7 @@ grouped_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                         } else {
                             tma_load_3d(sw + j * (S_W_BYTES / S), &g.tm_w, &full_bar[stage], k, m0, x.e);
                         }
-                        tma_load_2d(sx + j * nb * GK * 2, &g.tm_x, &full_bar[stage], k, x.t0);
+                        tma_load_2d(sx + j * nb * GK * 2, &g.tm_t[high], &full_bar[stage], k, x.t0);
                     }
                     ++sent;
                     if (++stage == stages) { stage = 0; phase ^= 1u; }
@@ -1717,10 +1721,10 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
 
     if (!one_round && p->T > kPairFrom * p->E) {
         if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, w_rows) ||
-            !encode(&g.tm_x, p->type, x, g.K, p->T, ld_x, 0, 0, 128) ||
-            !encode(&g.tm_out, p->type, x, g.K, p->T, ld_x, 0, 0, 64) ||
             !encode(&g.tm_y, p->type, g.out, g.M, p->T, g.ld_out, 0, 0, 16, 256))
             return SF_ERR_CUDA;
+        for (int b = 0; b < 4; ++b)
+            if (!encode(&g.tm_t[b], p->type, x, g.K, p->T, ld_x, 0, 0, 32 * (b + 1))) return SF_ERR_CUDA;
         const int slots = pair_slots();
         if (slots <= 0) return SF_ERR_CUDA;
         const int64_t most = ((int64_t)p->T / 64 + p->E) * ((g.M + PM - 1) / PM);
@@ -1747,9 +1751,9 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
     g.stages = (units * g.split <= (g.split > 1 ? sms * 3 / 4 : sms) ? 200 : 100) * 1024 / stage_bytes;
     if (g.stages > S_MAX_STAGES) g.stages = S_MAX_STAGES;
     const int box_rows = fwd ? rows : 64, box_bytes = !fwd && s == 4 ? 64 : 128;
-    if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, box_rows, box_bytes) ||
-        !encode(&g.tm_x, p->type, x, g.K, p->T, ld_x, 0, 0, nb))
-        return SF_ERR_CUDA;
+    if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, box_rows, box_bytes)) return SF_ERR_CUDA;
+    for (int b = 0; 16 << b <= nb; ++b)
+        if (!encode(&g.tm_t[b], p->type, x, g.K, p->T, ld_x, 0, 0, 16 << b)) return SF_ERR_CUDA;
     auto kernel = rounds ? grouped_small_kernel<TRANS, 1, true> : s == 1 ? grouped_small_kernel<TRANS, 1, false>
                   : s == 2 ? grouped_small_kernel<TRANS, 2, false> : grouped_small_kernel<TRANS, 4, false>;
     const int grid = (int)(rounds ? 2 * sms : units * g.split);
