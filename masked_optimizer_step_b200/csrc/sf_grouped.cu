@@ -43,10 +43,10 @@ constexpr int T_OUT_BYTES = 32 * 128 * 2;     // forward, dx: 2 x 16 tokens' row
 constexpr int W_OUT_BYTES = 32 * 128;         // weight gradient: 32 rows of 128 bytes of a warp's output
 constexpr size_t T_SMEM_BYTES = (size_t)T_RING_BYTES + 2 * T_OUT_BYTES + 1024;
 // weight gradient: 256 columns to a tile, two accumulators that the MMAs and the epilogue take in turn
-constexpr int W_STAGES_NEW = 6, W_STAGES_OLD = 3;
+constexpr int W_STAGES_NEW = 6, W_STAGES_FEW = 3;
 constexpr int W_STAGE_BYTES = 2 * P_HALF_BYTES;
 constexpr size_t W_SMEM_BYTES = (size_t)W_STAGES_NEW * W_STAGE_BYTES + P_EPI_WARPS * W_OUT_BYTES + 1024;
-static_assert(W_SMEM_BYTES == (size_t)W_STAGES_OLD * W_STAGE_BYTES + P_EPI_WARPS * 4 * W_OUT_BYTES + 1024, "both divisions");
+static_assert(W_SMEM_BYTES == (size_t)W_STAGES_FEW * W_STAGE_BYTES + P_EPI_WARPS * 4 * W_OUT_BYTES + 1024, "both divisions");
 constexpr int T_AHEAD = 3;                    // stages of a unit whose first halves run before any second half
 constexpr int T_BAND = 4;                     // token tiles that share a pass over an expert's weights
 
@@ -889,12 +889,14 @@ __device__ __forceinline__ bool has_tail(const WUnit &x) { return (x.cnt & (G_UM
 // OLD: for gradients that are added to, over few tokens. What W holds comes into the output boxes by TMA while the MMAs
 // run, is added there and goes out by TMA: the time is that of reading and writing W once, with fewer stages for the
 // tokens and a place for all of a warp's boxes. Otherwise the addition is TMA's, at 2.4 TB/s of results.
-template <bool OLD>
+// FEW: the same division of the shared memory for few tokens without OLD, where a unit's time is that of its way out.
+template <bool OLD, bool FEW>
 __global__ void __launch_bounds__(W_THREADS, 1)
 grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 {
-    constexpr int W_STAGES = OLD ? W_STAGES_OLD : W_STAGES_NEW;
-    constexpr int BOXES = OLD ? 4 : 1;          // output boxes of a warp in shared memory
+    static_assert(FEW || !OLD, "what W holds takes all of a warp's boxes");
+    constexpr int W_STAGES = FEW ? W_STAGES_FEW : W_STAGES_NEW;
+    constexpr int BOXES = FEW ? 4 : 1;          // output boxes of a warp in shared memory
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full_bar[W_STAGES], empty_bar[W_STAGES], tfull_bar[2], tempty_bar[2], drain_bar;
     __shared__ uint64_t tail_bar[W_STAGES], clear_bar[W_STAGES];   // for the last stage of an expert, where rows are cleared
@@ -1165,9 +1167,9 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     if (q >= boxes) break;
-                    uint8_t *s_out = s_warp + (OLD ? q * W_OUT_BYTES : 0);
+                    uint8_t *s_out = s_warp + (FEW ? q * W_OUT_BYTES : 0);
                     float4 *slot = reinterpret_cast<float4 *>(s_out) + lane * 8;
-                    if (!OLD) {
+                    if (!FEW || (!OLD && q == 0)) {
                         if (lane == 0) bulk_wait_read<0>();
                         __syncwarp();
                     }
@@ -1192,10 +1194,12 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     if (2 * q >= boxes) break;
-                    uint8_t *s_out = s_warp;
+                    uint8_t *s_out = s_warp + (FEW ? q * W_OUT_BYTES : 0);
                     uint4 *slot = reinterpret_cast<uint4 *>(s_out) + lane * 8;
-                    if (lane == 0) bulk_wait_read<0>();
-                    __syncwarp();
+                    if (!FEW || q == 0) {
+                        if (lane == 0) bulk_wait_read<0>();
+                        __syncwarp();
+                    }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         uint32_t w[4];
@@ -1682,6 +1686,10 @@ constexpr int64_t kPairFrom = 96;
 // on the addition is TMA's. 4 experts of 11008 x 4096 over 64, 256, 512 and 900 tokens each: 250, 259, 313 and 509 us the
 // one way, 322, 327, 330 and 418 us the other.
 constexpr int64_t kDwOldBelow = 512;
+// dw that does not add: below this many, fewer stages and a place for all of a warp's boxes too. At 16, 64, 128 and 512
+// tokens, so against with the deep ring: 56 / 77, 61 / 78, 71 / 72 and 102 / 90 us for 16 experts of 2048 x 2048; 133 / 144,
+// 140 / 147, 159 / 154 and 254 / 209 us for 4 of 11008 x 4096.
+constexpr int64_t kDwFewBelow = 128;
 
 template <bool TRANS>
 int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
@@ -1813,8 +1821,9 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
             return SF_ERR_CUDA;
         const int slots = pair_slots();
         if (slots <= 0) return SF_ERR_CUDA;
-        const bool old = accumulate && p->T < kDwOldBelow * p->E;
-        return launch(old ? grouped_dw_kernel<true> : grouped_dw_kernel<false>,
+        const bool few = p->T < (accumulate ? kDwOldBelow : kDwFewBelow) * p->E;
+        auto kernel = !few ? grouped_dw_kernel<false, false> : accumulate ? grouped_dw_kernel<true, true> : grouped_dw_kernel<false, true>;
+        return launch(kernel,
                       2 * (int)(pair_units < slots ? pair_units : slots), 2, W_THREADS, W_SMEM_BYTES, g, dev_status, stream);
     }
     // Tokens in slices while the units still fit the device at once (one expert of 512 x 512 over 8,192 tokens: 102, 43 and

@@ -153,6 +153,24 @@ def test_few_weights_and_many_tokens(sf, counts, R, C, out, add):
     assert int(status) == 0
 
 
+@pytest.mark.parametrize("counts", [[5, 0, 64, 16, 1, 33, 127, 100], [1] * 20, [300, 2, 0, 9, 31, 80, 200, 17]])
+@pytest.mark.parametrize("out,add", [(F32, False), (F32, True), (BF, False)])
+def test_large_weight_gradients_of_few_tokens(sf, counts, out, add):
+    """Many tiles of W to a handful of tokens: what counts is the results' way out, tile by tile."""
+    R, C = 1288, 1800
+    off, T, E, status = offsets(counts), sum(counts), len(counts), sf.status_word()
+    A, Y, G = normal(T, C, seed=17), normal(T, R, seed=18), normal(E, R + 8, C + 16, dt=out, seed=19)
+    old = G.clone()
+    sf.sf_grouped_dw(sf.grouped_problem(A, G[:, :R, :C], Y, off), status, accumulate=add)
+    for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+        before = old[e, :R, :C].double() if add else torch.zeros(R, C, dtype=torch.float64, device=DEV)
+        y, x = Y[a:b].double(), A[a:b].double()
+        ref, size = y.t() @ x + before, y.abs().t() @ x.abs() + before.abs()
+        slack = ((b - a) / 16 + 32) * 2.0 ** -23 * size
+        assert bool(((G[e, :R, :C].double() - ref).abs() <= slack + torch.finfo(out).eps / 2 * (ref.abs() + slack)).all())
+    assert torch.equal(G[:, R:], old[:, R:]) and torch.equal(G[:, :, C:], old[:, :, C:]) and int(status) == 0
+
+
 def chain(sf, T=700, E=5, R=520, C=264, seed=0):
     """Forward, gradients, norm and step of one expert projection: every call reads what the one before wrote."""
     W, A, dY = normal(E, R, C, dt=F32, seed=seed) * 0.05, normal(T, C, seed=seed + 1), normal(T, R, seed=seed + 2) * 0.01
