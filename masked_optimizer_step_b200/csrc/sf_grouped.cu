@@ -84,6 +84,7 @@ struct GArgs {
     int32_t nb, stages;              // single CTAs: token box, stages
     int32_t split;                   // single CTAs in slices: CTAs (a cluster) that share a unit's K
     int32_t out_f32, accumulate;     // dw
+    int32_t whole;                   // dw: tm_t[0] (bit 0) and tm_t[1] (bit 1) have Y and A by chunks of 64 columns
 };
 
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lbo, uint32_t sbo)
@@ -999,10 +1000,18 @@ grouped_dw_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                         tails |= 1u << stage;
                     } else {
                         if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * W_STAGE_BYTES);
-                        tma_load_2d_pair(sy, &g.tm_x, &full_bar[stage], r, t);
-                        tma_load_2d_pair(sy + G_BOX_BYTES, &g.tm_x, &full_bar[stage], r + 64, t);
-                        tma_load_2d_pair(sa, &g.tm_w, &full_bar[stage], c, t);
-                        tma_load_2d_pair(sa + G_BOX_BYTES, &g.tm_w, &full_bar[stage], c + 64, t);
+                        if (g.whole & 1) {
+                            tma_load_3d_pair(sy, &g.tm_t[0], &full_bar[stage], 0, t, r / 64);
+                        } else {
+                            tma_load_2d_pair(sy, &g.tm_x, &full_bar[stage], r, t);
+                            tma_load_2d_pair(sy + G_BOX_BYTES, &g.tm_x, &full_bar[stage], r + 64, t);
+                        }
+                        if (g.whole & 2) {
+                            tma_load_3d_pair(sa, &g.tm_t[1], &full_bar[stage], 0, t, c / 64);
+                        } else {
+                            tma_load_2d_pair(sa, &g.tm_w, &full_bar[stage], c, t);
+                            tma_load_2d_pair(sa + G_BOX_BYTES, &g.tm_w, &full_bar[stage], c + 64, t);
+                        }
                     }
                     issued[stage] = true;
                     issued_parity[stage] = phase;
@@ -1365,11 +1374,19 @@ grouped_dw_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                     for (int j = 0; j < S; ++j) {
                         // a step behind the end reads behind the last row: zeros
                         const int t = tokens_of(j, i) > 0 ? t0 + (step0 + j * nk + i) * GK : g.T;
-                        tma_load_2d(sy + j * (P_HALF_BYTES / S), &g.tm_x, &full_bar[stage], r0, t);
-                        if (S == 1) tma_load_2d(sy + G_BOX_BYTES, &g.tm_x, &full_bar[stage], r0 + 64, t);
+                        if (S == 1 && (g.whole & 1)) {
+                            tma_load_3d(sy, &g.tm_t[0], &full_bar[stage], 0, t, r0 / 64);
+                        } else {
+                            tma_load_2d(sy + j * (P_HALF_BYTES / S), &g.tm_x, &full_bar[stage], r0, t);
+                            if (S == 1) tma_load_2d(sy + G_BOX_BYTES, &g.tm_x, &full_bar[stage], r0 + 64, t);
+                        }
+                        if (S == 1 && (g.whole & 2)) {
+                            tma_load_3d(sa, &g.tm_t[1], &full_bar[stage], 0, t, c0 / 64);
+                        } else {
 #pragma unroll
-                        for (int b = 0; b < COLS / 64; ++b)
-                            tma_load_2d(sa + (j * (COLS / 64) + b) * G_BOX_BYTES, &g.tm_w, &full_bar[stage], c0 + 64 * b, t);
+                            for (int b = 0; b < COLS / 64; ++b)
+                                tma_load_2d(sa + (j * (COLS / 64) + b) * G_BOX_BYTES, &g.tm_w, &full_bar[stage], c0 + 64 * b, t);
+                        }
                     }
                     ++sent;
                     if (++stage == stages) { stage = 0; phase ^= 1u; }
@@ -1588,6 +1605,20 @@ bool encode(CUtensorMap *m, int type, const void *base, int cols, int64_t rows, 
                                  : CU_TENSOR_MAP_SWIZZLE_NONE,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
+}
+
+// Rows of whole chunks of 64 16-bit columns, as {64, rows, chunks}: a box is 64 rows of several chunks, each of which lies as a
+// box of its own would.
+bool encode_chunks(CUtensorMap *m, int type, const void *base, int cols, int64_t rows, int64_t ld, int chunks)
+{
+    EncodeTiledFn fn = grouped_encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(cols / 64)};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, 128};
+    const cuuint32_t box[3] = {64, 64, (cuuint32_t)chunks}, estr[3] = {1, 1, 1};
+    return fn(m, type == SF_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base),
+              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int check_grouped(const sf_grouped *p, bool dw)
@@ -1821,6 +1852,10 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
             return SF_ERR_CUDA;
         const int slots = pair_slots();
         if (slots <= 0) return SF_ERR_CUDA;
+        // Where the columns are whole chunks of 64, one box takes two chunks: half the copies to issue (4 experts of 4096 x
+        // 4096 over 1,024 tokens and more: 2% less).
+        if (p->T > 0 && p->R % 64 == 0 && encode_chunks(&g.tm_t[0], p->type, y, p->R, p->T, ld_y, 2)) g.whole |= 1;
+        if (p->T > 0 && p->C % 64 == 0 && encode_chunks(&g.tm_t[1], p->type, a, p->C, p->T, ld_a, 2)) g.whole |= 2;
         const bool few = p->T < (accumulate ? kDwOldBelow : kDwFewBelow) * p->E;
         auto kernel = !few ? grouped_dw_kernel<false, false> : accumulate ? grouped_dw_kernel<true, true> : grouped_dw_kernel<false, true>;
         return launch(kernel,
@@ -1840,6 +1875,9 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
     if (!encode(&g.tm_w, p->type, a, p->C, p->T, ld_a, 0, 0, 64) ||
         !encode(&g.tm_x, p->type, y, p->R, p->T, ld_y, 0, 0, 64, s == 4 ? 64 : 128))
         return SF_ERR_CUDA;
+    // 2 copies a stage in place of 6 (8 experts of 1024 x 1024 over 128 tokens each: 11.7 -> 10.4 us; with slices no gain)
+    if (p->T > 0 && s == 1 && p->R % 64 == 0 && encode_chunks(&g.tm_t[0], p->type, y, p->R, p->T, ld_y, 2)) g.whole |= 1;
+    if (p->T > 0 && s == 1 && p->C % 64 == 0 && encode_chunks(&g.tm_t[1], p->type, a, p->C, p->T, ld_a, 4)) g.whole |= 2;
     auto kernel = g.split > 1 ? grouped_dw_small_kernel<4, true> : s == 1 ? grouped_dw_small_kernel<1, false>
                   : s == 2 ? grouped_dw_small_kernel<2, false> : grouped_dw_small_kernel<4, false>;
     return launch(kernel, (int)units * g.split, g.split, D_THREADS, (size_t)g.stages * D_STAGE_BYTES + 1024, g, dev_status, stream);
