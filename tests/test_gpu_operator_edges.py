@@ -171,6 +171,26 @@ def test_large_weight_gradients_of_few_tokens(sf, counts, out, add):
     assert torch.equal(G[:, R:], old[:, R:]) and torch.equal(G[:, :, C:], old[:, :, C:]) and int(status) == 0
 
 
+@pytest.mark.parametrize("counts,R,C", [([700, 301, 64], 2112, 1600), ([1300, 0, 977], 1856, 2048), ([40, 3, 0, 120], 2112, 1600), ([130] * 8, 1088, 960),
+                                        ([5, 64, 31, 0, 128, 1], 832, 1344), ([2000], 320, 4160), ([130] * 8, 1088, 968), ([700, 301], 2120, 1600)])
+@pytest.mark.parametrize("out,add", [(F32, False), (F32, True), (BF, False)])
+def test_weight_gradients_of_whole_and_broken_chunks(sf, counts, R, C, out, add):
+    """Columns in whole chunks of 64, and not, with last tiles of every width; rows that are views of wider ones."""
+    off, T, E, status = offsets(counts), sum(counts), len(counts), sf.status_word()
+    wide_a, wide_y = torch.full((T + 1, C + 72), float("nan"), dtype=BF, device=DEV), torch.full((T + 1, R + 8), float("nan"), dtype=BF, device=DEV)
+    A, Y, G = wide_a[:T, :C], wide_y[:T, :R], normal(E, R, C, dt=out, seed=22)
+    A.copy_(normal(T, C, seed=20))
+    Y.copy_(normal(T, R, seed=21))
+    old = G.double() if add else torch.zeros(E, R, C, dtype=torch.float64, device=DEV)
+    sf.sf_grouped_dw(sf.grouped_problem(A, G, Y, off), status, accumulate=add)
+    for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+        y, x = Y[a:b].double(), A[a:b].double()
+        ref, size = y.t() @ x + old[e], y.abs().t() @ x.abs() + old[e].abs()
+        slack = ((b - a) / 16 + 32) * 2.0 ** -23 * size
+        assert bool(((G[e].double() - ref).abs() <= slack + torch.finfo(out).eps / 2 * (ref.abs() + slack)).all())
+    assert int(status) == 0
+
+
 def chain(sf, T=700, E=5, R=520, C=264, seed=0):
     """Forward, gradients, norm and step of one expert projection: every call reads what the one before wrote."""
     W, A, dY = normal(E, R, C, dt=F32, seed=seed) * 0.05, normal(T, C, seed=seed + 1), normal(T, R, seed=seed + 2) * 0.01
