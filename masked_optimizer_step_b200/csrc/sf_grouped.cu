@@ -1586,7 +1586,7 @@ EncodeTiledFn grouped_encode_fn()
     return fn;
 }
 
-// Map over [depth x rows x cols] (depth 0: two dimensions) with boxes of box_bytes (128 or 64, swizzled) by box_rows rows.
+// Map over [depth x rows x cols] (depth 0: two dimensions) with boxes of box_bytes (128 or 64, swizzled, or 256, plain) by box_rows rows.
 bool encode(CUtensorMap *m, int type, const void *base, int cols, int64_t rows, int64_t ld, int depth, int64_t stride,
             int box_rows, int box_bytes = 128)
 {
