@@ -546,7 +546,8 @@ class Dense:
 
 
 class DenseTensors:
-    """The argument array of a list of dense_tensor() descriptors, built once for many steps."""
+    """The argument array of a list of dense_tensor() descriptors, built once for many steps. It holds the tensors' addresses:
+    gradients are to be written in place (zeroed, not dropped and made anew) from step to step."""
 
     def __init__(self, tensors):
         self.descs = [t.desc() if isinstance(t, Dense) else t for t in tensors]
@@ -612,6 +613,8 @@ def grouped_problem(A, W, Y, offsets) -> Desc:
     (T, C), (E, R) = A.shape, W.shape[:2]
     if W.shape[2] != C or tuple(Y.shape) != (T, R):
         raise ValueError(f"shapes do not match: A {tuple(A.shape)}, W {tuple(W.shape)}, Y {tuple(Y.shape)}")
+    if max(E, T, R, C) >= 2 ** 31:
+        raise ValueError("sizes are 32-bit")
     for name, t in (("A", A), ("W", W), ("Y", Y)):
         if t.numel() and t.stride(-1) != 1:
             raise ValueError(f"{name}: columns must be contiguous")

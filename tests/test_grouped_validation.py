@@ -101,3 +101,11 @@ def test_binding_refuses_host_tensors():
     w = torch.zeros((2, 8, 8), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         b.grouped_problem(x, w, x, torch.zeros(3, dtype=torch.int32))
+
+
+def test_binding_refuses_sizes_beyond_32_bits():
+    def meta(*shape):
+        return torch.empty(shape, dtype=torch.bfloat16, device="meta")
+    off = torch.zeros(3, dtype=torch.int32, device="meta")
+    with pytest.raises(ValueError, match="32-bit"):
+        b.grouped_problem(meta(2 ** 32 + 8, 8), meta(2, 16, 8), meta(2 ** 32 + 8, 16), off)
