@@ -1709,10 +1709,11 @@ int launch(K kernel, int grid, int cluster, int threads, size_t smem, const GArg
 
 // Forward, dx: pairs run when an expert has more than this many tokens on average. At 96, 128 and 256 of them, single CTAs
 // against pairs: 50.6 / 64.5, 70.6 / 65.9 and 98 / 76 us for 8 experts of 4096 x 4096; 69.8 / 74.4, 96 / 79 and 158 / 101 us
-// for 48 of 1416 x 2056; 258 / 299, 308 / 340 and 455 / 369 us for 16 of 11008 x 4096. With short sums they cross later
-// (64 experts of 1024 x 1024: 32 / 44, 37 / 46, 52 / 56 us), with unevenly filled experts sooner (48 of 1416 x 2056 over 96
-// tokens each on average: 88 / 66 us).
-constexpr int64_t kPairFrom = 96;
+// for 48 of 1416 x 2056; 258 / 299, 308 / 340 and 455 / 369 us for 16 of 11008 x 4096. Short sums (nk steps of 64) have less
+// to gain from large tiles: 8 experts of 4096 x 256 over 100, 200, 300 and 800 tokens each 9.6 / 13.5, 13.9 / 15.3, 18.0 /
+// 19.3 and 33.9 / 32.5 us, 32 of 1376 x 512 over 128 and 300 15.8 / 18.8 and 25.6 / 30.5; 64 of 1024 x 1024 over 100, 160
+// and 250 32.4 / 40.7, 40.9 / 43.8 and 50.6 / 51.0.
+constexpr int64_t pair_from(int nk) { return nk <= 8 ? 512 : nk <= 16 ? 192 : 96; }
 // dw that adds: below this many tokens to an expert, what W holds comes in by TMA and is added in shared memory; from there
 // on the addition is TMA's. 4 experts of 11008 x 4096 over 64, 256, 512 and 900 tokens each: 250, 259, 313 and 509 us the
 // one way, 322, 327, 330 and 418 us the other.
@@ -1758,7 +1759,7 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
     const int64_t m_tiles = (g.M + SM_ROWS - 1) / SM_ROWS;
     const bool one_round = tiles * m_tiles <= 2 * sms;
 
-    if (!one_round && p->T > kPairFrom * p->E) {
+    if (!one_round && p->T > pair_from(nk) * p->E) {
         if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, w_rows) ||
             !encode(&g.tm_y, p->type, g.out, g.M, p->T, g.ld_out, 0, 0, 16, 256))
             return SF_ERR_CUDA;
