@@ -1771,9 +1771,14 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
         const int pairs = (int)(most < slots ? most : slots);
         return launch(grouped_pair_kernel<TRANS>, 2 * pairs, 2, P_THREADS, T_SMEM_BYTES, g, status, stream);
     }
-    // K in slices while an expert's tokens fit one tile and the units fit the device at once, two CTAs to an SM
+    // K in slices while the units fit the device at once, two CTAs to an SM, with a token tile to an expert where most experts'
+    // tokens fit one. Where they take several, only long sums that leave half of the SMs without work (one expert of 64 x 4096
+    // over 300, 1,000 and 8,000 tokens: 23.8, 24.4 and 25.2 us without slices, 8.4, 9.2 and 15.3 with; 3 of 88 x 560 over 416
+    // each 8.9 / 9.5, one of 184 x 9632 over 7,202 53 / 69).
+    const bool one_tile = avg <= nb;
     int s = 1;
-    while (s < 4 && avg <= nb && busy * m_tiles * 2 * s <= 2 * sms && nk >= 4 * s && 2 * s * nb <= 256) s *= 2;
+    while (s < 4 && (one_tile ? busy * m_tiles <= sms / s : tiles * m_tiles <= sms / (2 * s)) && nk >= (one_tile ? 4 : 10) * s && 2 * s * nb <= 256)
+        s *= 2;
     g.nb = nb;
     // Several units to a CTA, planned ahead, where a unit is short (64 experts of 1024 x 1024 over 64 tokens each: 35.6 ->
     // 32.1 us); long ones come out more even as a CTA each (the decode batch above: 114.6 against 117.5 us).

@@ -119,7 +119,8 @@ def test_tiles_of_every_width(sf, counts, dt):
 
 @pytest.mark.parametrize("counts,M,K", [([1], 64, 4096), ([16], 72, 4104), ([42], 248, 7912), ([100], 520, 11008), ([3, 0, 9, 4], 64, 4096),
                                         ([2, 2], 1032, 4096), ([100, 0, 90], 264, 2568), ([2], 4096, 4096), ([0, 1, 0], 8, 8200),
-                                        ([10, 22, 1, 0, 30, 64, 17, 8], 64, 2056), ([17] * 32, 64, 2048)])
+                                        ([10, 22, 1, 0, 30, 64, 17, 8], 64, 2056), ([17] * 32, 64, 2048),
+                                        ([232, 232], 184, 3784), ([541], 1472, 5608), ([1000], 64, 4096), ([300, 0, 700, 129], 72, 2056)])
 @pytest.mark.parametrize("dt", [BF, torch.float16])
 def test_few_rows_and_long_sums(sf, counts, M, K, dt):
     """Few results over a long K, whose slices are spread over SMs."""
