@@ -16,7 +16,7 @@ own = False
 DEV = "cuda"
 BLOCK = 256                       # elements that share one scale of the 8-bit moments
 LR, BETA1, BETA2, EPS, WD, MAX_NORM = 1e-4, 0.9, 0.95, 1e-8, 0.1, 1.0
-STEPS_BEFORE, T_MAX = 100, 20000
+STEPS_BEFORE, T_MAX = 100, 2000
 SCALE_FLOOR = 2.0 ** -100         # smallest scale of a block
 LAYER = (4096 * 4096,) * 4 + (11008 * 4096,) * 3
 
