@@ -1682,11 +1682,17 @@ int pair_slots()
     return n;
 }
 
+// Lets the kernel have `smem` bytes of shared memory. Called before the tensor maps are made: in a host thread's first call
+// it is what makes the device's context current, without which no map can be encoded.
+template <typename K>
+bool prepare_kernel(K kernel, size_t smem)
+{
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+}
+
 template <typename K>
 int launch(K kernel, int grid, int cluster, int threads, size_t smem, const GArgs &g, uint32_t *status, sf_stream stream)
 {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return SF_ERR_CUDA;
     // programmatic dependent launch: the kernels wait for their predecessor themselves, behind what they can do without it
     // (4.4 -> 3.4 us for the smallest calls back to back)
     cudaLaunchAttribute attr[2];
@@ -1760,6 +1766,7 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
     const bool one_round = tiles * m_tiles <= 2 * sms;
 
     if (!one_round && p->T > pair_from(nk) * p->E) {
+        if (!prepare_kernel(grouped_pair_kernel<TRANS>, T_SMEM_BYTES)) return SF_ERR_CUDA;
         if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, w_rows) ||
             !encode(&g.tm_y, p->type, g.out, g.M, p->T, g.ld_out, 0, 0, 16, 256))
             return SF_ERR_CUDA;
@@ -1796,13 +1803,15 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
     g.stages = (units * g.split <= (g.split > 1 ? sms * 3 / 4 : sms) ? 200 : 100) * 1024 / stage_bytes;
     if (g.stages > S_MAX_STAGES) g.stages = S_MAX_STAGES;
     const int box_rows = fwd ? rows : 64, box_bytes = !fwd && s == 4 ? 64 : 128;
+    auto kernel = rounds ? grouped_small_kernel<TRANS, 1, true> : s == 1 ? grouped_small_kernel<TRANS, 1, false>
+                  : s == 2 ? grouped_small_kernel<TRANS, 2, false> : grouped_small_kernel<TRANS, 4, false>;
+    const size_t smem = (size_t)g.stages * stage_bytes + 1024;
+    if (!prepare_kernel(kernel, smem)) return SF_ERR_CUDA;
     if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, box_rows, box_bytes)) return SF_ERR_CUDA;
     for (int b = 0; 16 << b <= nb; ++b)
         if (!encode(&g.tm_t[b], p->type, x, g.K, p->T, ld_x, 0, 0, 16 << b)) return SF_ERR_CUDA;
-    auto kernel = rounds ? grouped_small_kernel<TRANS, 1, true> : s == 1 ? grouped_small_kernel<TRANS, 1, false>
-                  : s == 2 ? grouped_small_kernel<TRANS, 2, false> : grouped_small_kernel<TRANS, 4, false>;
     const int grid = (int)(rounds ? 2 * sms : units * g.split);
-    return launch(kernel, grid, g.split, S_THREADS, (size_t)g.stages * stage_bytes + 1024, g, status, stream);
+    return launch(kernel, grid, g.split, S_THREADS, smem, g, status, stream);
 }
 
 }  // namespace
@@ -1853,6 +1862,9 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
     // over 128 tokens each: 11.1 us against 13.1; one of 2048 x 2048 over 4,096: 56 us against 30).
     const bool one_round = busy * tiles(SM_ROWS, PN) <= 2 * sms && p->T <= (int64_t)512 * p->E;
     if (busy * tiles(PM, PN) >= sms / 4 && !one_round) {
+        const bool few = p->T < (accumulate ? kDwOldBelow : kDwFewBelow) * p->E;
+        auto kernel = !few ? grouped_dw_kernel<false, false> : accumulate ? grouped_dw_kernel<true, true> : grouped_dw_kernel<false, true>;
+        if (!prepare_kernel(kernel, W_SMEM_BYTES)) return SF_ERR_CUDA;
         if (!encode(&g.tm_w, p->type, a, p->C, p->T, ld_a, 0, 0, 64) || !encode(&g.tm_x, p->type, y, p->R, p->T, ld_y, 0, 0, 64) ||
             !encode(&g.tm_out, p->w_type, p->W, p->C, p->R, p->ld_w, p->E, stride, 32))
             return SF_ERR_CUDA;
@@ -1862,8 +1874,6 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
         // 4096 over 1,024 tokens and more: 2% less).
         if (p->T > 0 && p->R % 64 == 0 && encode_chunks(&g.tm_t[0], p->type, y, p->R, p->T, ld_y, 2)) g.whole |= 1;
         if (p->T > 0 && p->C % 64 == 0 && encode_chunks(&g.tm_t[1], p->type, a, p->C, p->T, ld_a, 2)) g.whole |= 2;
-        const bool few = p->T < (accumulate ? kDwOldBelow : kDwFewBelow) * p->E;
-        auto kernel = !few ? grouped_dw_kernel<false, false> : accumulate ? grouped_dw_kernel<true, true> : grouped_dw_kernel<false, true>;
         return launch(kernel,
                       2 * (int)(pair_units < slots ? pair_units : slots), 2, W_THREADS, W_SMEM_BYTES, g, dev_status, stream);
     }
@@ -1878,13 +1888,15 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
     const int64_t units = p->E * tiles(SM_ROWS / s, PN / s);
     while (s == 4 && g.split < 8 && units * 2 * g.split <= sms && p->T > (int64_t)4 * GK * 4 * 2 * g.split * p->E) g.split *= 2;
     g.stages = units * g.split <= (g.split > 1 ? sms * 3 / 4 : sms) ? 4 : 2;       // one CTA to an SM, or two
+    auto kernel = g.split > 1 ? grouped_dw_small_kernel<4, true> : s == 1 ? grouped_dw_small_kernel<1, false>
+                  : s == 2 ? grouped_dw_small_kernel<2, false> : grouped_dw_small_kernel<4, false>;
+    const size_t smem = (size_t)g.stages * D_STAGE_BYTES + 1024;
+    if (!prepare_kernel(kernel, smem)) return SF_ERR_CUDA;
     if (!encode(&g.tm_w, p->type, a, p->C, p->T, ld_a, 0, 0, 64) ||
         !encode(&g.tm_x, p->type, y, p->R, p->T, ld_y, 0, 0, 64, s == 4 ? 64 : 128))
         return SF_ERR_CUDA;
     // 2 copies a stage in place of 6 (8 experts of 1024 x 1024 over 128 tokens each: 11.7 -> 10.4 us; with slices no gain)
     if (p->T > 0 && s == 1 && p->R % 64 == 0 && encode_chunks(&g.tm_t[0], p->type, y, p->R, p->T, ld_y, 2)) g.whole |= 1;
     if (p->T > 0 && s == 1 && p->C % 64 == 0 && encode_chunks(&g.tm_t[1], p->type, a, p->C, p->T, ld_a, 4)) g.whole |= 2;
-    auto kernel = g.split > 1 ? grouped_dw_small_kernel<4, true> : s == 1 ? grouped_dw_small_kernel<1, false>
-                  : s == 2 ? grouped_dw_small_kernel<2, false> : grouped_dw_small_kernel<4, false>;
-    return launch(kernel, (int)units * g.split, g.split, D_THREADS, (size_t)g.stages * D_STAGE_BYTES + 1024, g, dev_status, stream);
+    return launch(kernel, (int)units * g.split, g.split, D_THREADS, smem, g, dev_status, stream);
 }
