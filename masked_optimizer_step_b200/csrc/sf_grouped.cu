@@ -56,9 +56,12 @@ constexpr int S_EPI_WARPS = 4;
 constexpr int S_THREADS = 64 + 32 * S_EPI_WARPS;
 constexpr int S_W_BYTES = SM_ROWS * GK * 2;   // 16 KB
 constexpr int S_MAX_STAGES = 12;
+constexpr int S_RING_BYTES = 200 * 1024;      // stages of a CTA that has its SM to itself, at most; half for two to an SM
+constexpr size_t S_SMEM_BYTES = (size_t)S_RING_BYTES + 1024;
 constexpr int D_THREADS = P_THREADS;          // weight gradient: TMA, MMA and eight epilogue warps
 constexpr int D_STAGE_BYTES = 3 * P_HALF_BYTES;
 constexpr int D_MAX_STAGES = 4;
+constexpr size_t D_SMEM_BYTES = (size_t)D_MAX_STAGES * D_STAGE_BYTES + 1024;
 
 // Weight gradient, fp32: tokens that the tensor core sums before the sums are added in fp32, in stages. It adds with
 // truncation, so the error grows with the length (relative, normal values: 2.3e-7, 9.9e-7 and 9.1e-6 at 256, 1,024
@@ -1682,12 +1685,13 @@ int pair_slots()
     return n;
 }
 
-// Lets the kernel have `smem` bytes of shared memory. Called before the tensor maps are made: in a host thread's first call
-// it is what makes the device's context current, without which no map can be encoded.
+// Lets the kernel have the shared memory of the largest of its calls. The limit is one for all host threads, so it is never
+// set to a call's own size, which another thread's launch may be above. Called before the tensor maps are made: in a host
+// thread's first call it is what makes the device's context current, without which no map can be encoded.
 template <typename K>
-bool prepare_kernel(K kernel, size_t smem)
+bool prepare_kernel(K kernel, size_t most)
 {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) == cudaSuccess;
 }
 
 template <typename K>
@@ -1800,18 +1804,17 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
     while (s > 1 && g.split < 8 && units * 2 * g.split <= sms * 7 / 4 && nk >= 2 * 2 * g.split * s) g.split *= 2;
     // One CTA to an SM, or two. Clusters do not fill every SM (8 experts of 128 x 2048 over 2 tokens each, 144 CTAs in
     // clusters of 4: 7.9 us with one to an SM, 5.3 with two).
-    g.stages = (units * g.split <= (g.split > 1 ? sms * 3 / 4 : sms) ? 200 : 100) * 1024 / stage_bytes;
+    g.stages = (units * g.split <= (g.split > 1 ? sms * 3 / 4 : sms) ? S_RING_BYTES : S_RING_BYTES / 2) / stage_bytes;
     if (g.stages > S_MAX_STAGES) g.stages = S_MAX_STAGES;
     const int box_rows = fwd ? rows : 64, box_bytes = !fwd && s == 4 ? 64 : 128;
     auto kernel = rounds ? grouped_small_kernel<TRANS, 1, true> : s == 1 ? grouped_small_kernel<TRANS, 1, false>
                   : s == 2 ? grouped_small_kernel<TRANS, 2, false> : grouped_small_kernel<TRANS, 4, false>;
-    const size_t smem = (size_t)g.stages * stage_bytes + 1024;
-    if (!prepare_kernel(kernel, smem)) return SF_ERR_CUDA;
+    if (!prepare_kernel(kernel, S_SMEM_BYTES)) return SF_ERR_CUDA;
     if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, box_rows, box_bytes)) return SF_ERR_CUDA;
     for (int b = 0; 16 << b <= nb; ++b)
         if (!encode(&g.tm_t[b], p->type, x, g.K, p->T, ld_x, 0, 0, 16 << b)) return SF_ERR_CUDA;
     const int grid = (int)(rounds ? 2 * sms : units * g.split);
-    return launch(kernel, grid, g.split, S_THREADS, smem, g, status, stream);
+    return launch(kernel, grid, g.split, S_THREADS, (size_t)g.stages * stage_bytes + 1024, g, status, stream);
 }
 
 }  // namespace
@@ -1887,16 +1890,15 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
     // shorter sums or fewer slices clusters cost what they save).
     const int64_t units = p->E * tiles(SM_ROWS / s, PN / s);
     while (s == 4 && g.split < 8 && units * 2 * g.split <= sms && p->T > (int64_t)4 * GK * 4 * 2 * g.split * p->E) g.split *= 2;
-    g.stages = units * g.split <= (g.split > 1 ? sms * 3 / 4 : sms) ? 4 : 2;       // one CTA to an SM, or two
+    g.stages = units * g.split <= (g.split > 1 ? sms * 3 / 4 : sms) ? D_MAX_STAGES : D_MAX_STAGES / 2;       // one CTA to an SM, or two
     auto kernel = g.split > 1 ? grouped_dw_small_kernel<4, true> : s == 1 ? grouped_dw_small_kernel<1, false>
                   : s == 2 ? grouped_dw_small_kernel<2, false> : grouped_dw_small_kernel<4, false>;
-    const size_t smem = (size_t)g.stages * D_STAGE_BYTES + 1024;
-    if (!prepare_kernel(kernel, smem)) return SF_ERR_CUDA;
+    if (!prepare_kernel(kernel, D_SMEM_BYTES)) return SF_ERR_CUDA;
     if (!encode(&g.tm_w, p->type, a, p->C, p->T, ld_a, 0, 0, 64) ||
         !encode(&g.tm_x, p->type, y, p->R, p->T, ld_y, 0, 0, 64, s == 4 ? 64 : 128))
         return SF_ERR_CUDA;
     // 2 copies a stage in place of 6 (8 experts of 1024 x 1024 over 128 tokens each: 11.7 -> 10.4 us; with slices no gain)
     if (p->T > 0 && s == 1 && p->R % 64 == 0 && encode_chunks(&g.tm_t[0], p->type, y, p->R, p->T, ld_y, 2)) g.whole |= 1;
     if (p->T > 0 && s == 1 && p->C % 64 == 0 && encode_chunks(&g.tm_t[1], p->type, a, p->C, p->T, ld_a, 4)) g.whole |= 2;
-    return launch(kernel, (int)units * g.split, g.split, D_THREADS, smem, g, dev_status, stream);
+    return launch(kernel, (int)units * g.split, g.split, D_THREADS, (size_t)g.stages * D_STAGE_BYTES + 1024, g, dev_status, stream);
 }

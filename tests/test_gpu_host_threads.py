@@ -39,3 +39,50 @@ def test_the_first_call_of_a_thread(sf, product, E, T, R, C):
         check_dx(A, W, Y, off, A, BF)
     else:
         check_dw(A, G, Y, off, None, F32)
+
+
+def at_once(workers, calls):
+    """Runs every worker `calls` times in a thread and on a stream of its own; the errors they raised. A call drops Python's
+    lock while it is in the library, so one thread may be between a kernel's set-up and its launch while another sets up."""
+    errors, start = [], threading.Barrier(len(workers))
+
+    def loop(work):
+        stream = torch.cuda.Stream(device=DEV)
+        stream.synchronize()
+        start.wait()
+        try:
+            for _ in range(calls):
+                work(stream)
+        except Exception as e:
+            errors.append(e)
+        stream.synchronize()
+    threads = [threading.Thread(target=loop, args=(w,)) for w in workers]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return errors
+
+
+# one kernel with twice the shared memory for the first shape of each pair: few units, so a CTA has its SM to itself
+@pytest.mark.parametrize("shapes", [((1, 2, 256, 2048), (1, 2, 4096, 4096)), ((1, 60, 64, 4096), (2, 100, 2048, 2048))])
+def test_forward_calls_with_different_shared_memory(sf, shapes):
+    sets = []
+    for i, (E, T, R, C) in enumerate(shapes):
+        x = normal((T, C), BF, i), normal((E, R, C), BF, i + 5, 0.05), torch.zeros((T, R), dtype=BF, device=DEV), offsets([T // E] * E)
+        sets.append((x, sf.grouped_problem(*x)))
+    torch.cuda.synchronize()
+    assert not at_once([lambda s, p=p: sf.sf_grouped_forward(p, stream=s) for _, p in sets], 4000)
+    for (A, W, Y, off), _ in sets:
+        check_forward(A, W, Y, off, Y, BF)
+
+
+def test_weight_gradients_with_different_shared_memory(sf):
+    sets = []
+    for i, (T, R, C) in enumerate(((40, 128, 256), (40, 2048, 4096))):
+        x = normal((T, C), BF, i), torch.zeros((1, R, C), device=DEV), normal((T, R), BF, i + 5), offsets([T])
+        sets.append((x, sf.grouped_problem(*x)))
+    torch.cuda.synchronize()
+    assert not at_once([lambda s, p=p: sf.sf_grouped_dw(p, stream=s) for _, p in sets], 4000)
+    for (A, W, Y, off), _ in sets:
+        check_dw(A, W, Y, off, None, F32)
