@@ -336,10 +336,11 @@ int launch_embed(const int32_t *tokens, int n_tok, const void *dY, int H, int64_
     const size_t smem = index_smem_ints(n_tok, mk.slot_cap, keep_slots) * sizeof(int);
     if (smem > kSmemLimit) return SF_ERR_UNSUPPORTED;
     // above 48 KB of shared memory in all, static included, the launch needs the opt-in
-    // attribute; it is set from 40 KB of dynamic memory on (the static part is far below 8 KB)
+    // attribute; it is set from 40 KB of dynamic memory on (the static part is far below 8 KB), to the
+    // most that any call needs: the limit is one for all host threads
     if (smem > 40 * 1024 &&
         cudaFuncSetAttribute(embed_index_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem) != cudaSuccess)
+                             (int)kSmemLimit) != cudaSuccess)
         return SF_ERR_CUDA;
     const int sms = sm_count();
     if (sms <= 0) return SF_ERR_NO_DEVICE;

@@ -461,9 +461,10 @@ extern "C" int sf_sparse_update(const sf_matrix *mats, int n_mats, const sf_adam
 #endif
     const int unroll = SF_UPDATE_UNROLL;
     const void *fn = unroll == 2 ? (const void *)update_kernel<2> : (const void *)update_kernel<1>;
-    // opt-in beyond 48 KB of shared memory in all, static included (set from 40 KB dynamic on)
+    // opt-in beyond 48 KB of shared memory in all, static included (set from 40 KB dynamic on); the limit is one for all host
+    // threads, so it is never a call's own size, which another thread's launch may be above
     if (smem > 40 * 1024 &&
-        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kMaxC * sizeof(float))) != cudaSuccess)
         return SF_ERR_CUDA;
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, smem) != cudaSuccess ||

@@ -86,3 +86,18 @@ def test_weight_gradients_with_different_shared_memory(sf):
     assert not at_once([lambda s, p=p: sf.sf_grouped_dw(p, stream=s) for _, p in sets], 4000)
     for (A, W, Y, off), _ in sets:
         check_dw(A, W, Y, off, None, F32)
+
+
+def test_updates_with_different_shared_memory(sf):
+    """The update parks a row in shared memory: 44 KB for 11,008 columns, 64 KB for 16,384."""
+    sets = []
+    for C in (11008, 16384):
+        m = sf.Matrix(32, C, 32, DEV)
+        sf.sf_mask_init(m.mask)
+        sf.sf_quantize_init(normal((32, C), F32, C), m)
+        sf.sf_mask_update([m.mask], [sf.make_src(sf.SF_SRC_WORDS, torch.full((1,), -1, dtype=torch.int32, device=DEV))], 0.01)
+        m.grad.zero_()
+        sets.append((m, [sf.matrix_struct(m)], sf.AdamParams(lr=1e-3), sf.status_word()))
+    torch.cuda.synchronize()
+    assert not at_once([lambda s, x=x: sf.sf_sparse_update(x[1], x[2], x[3], stream=s) for x in sets], 4000)
+    assert all(int(x[3]) == 0 for x in sets)
