@@ -382,7 +382,7 @@ int sf_masked_dw_phase(const sf_dw_problem *probs /* host [n] */, int n, void *w
  * tensors of any lengths at once.
  * Per element, with f = factor[1] (1 when factor is NULL), t = step[0] + 1 and every operation
  * rounded in fp32 (the quotient is within 2 units in the last place):
- *   g  = clamp(grad * f, -clip, clip)                   (clip <= 0: no clamp)
+ *   g  = clamp(grad * f, -clip, clip)                   (clip <= 0: no clamp; a NaN stays one)
  *   m1 = beta1 * m + one_minus_b1 * g,   v1 = beta2 * v + one_minus_b2 * g * g
  *   u  = (m1 * bc1[t]) / (sqrt(v1) * sqrt(bc2[t]) + eps)
  *   p  = p - lr * u - (decay * lr * wd) * p             (p held in fp32, rounded once when bf16)
@@ -401,7 +401,8 @@ int sf_masked_dw_phase(const sf_dw_problem *probs /* host [n] */, int n, void *w
  * can overlap need step words of their own.
  * factor: the two floats of sf_grad_norm, or NULL. When factor[1] is 0 or NaN (the gradient was not
  * finite) the step is skipped: every tensor and the step count stay as they are, and
- * SF_STATUS_NONFINITE is set. A step that produces a non-finite weight or moment sets it too.
+ * SF_STATUS_NONFINITE is set. A step that produces a non-finite weight or moment sets it too, and so does
+ * one whose clip makes an infinite gradient finite.
  *
  * sf_grad_norm: out[0] = inv_scale * sqrt(sum of squares of every gradient of every tensor) (the squares
  * of eight elements summed in fp32, from there in fp64, in a fixed order), out[1] =

@@ -131,6 +131,15 @@ __device__ __forceinline__ pair_t ratio2(pair_t a, pair_t b)
     return mul2(a, pair_of(ya, yb));
 }
 
+// x between -limit and limit; a NaN stays one (fminf and fmaxf would take the limit in its place).
+__device__ __forceinline__ float clamped(float x, float limit)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(-limit));
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(r) : "f"(limit));
+    return r;
+}
+
 // A lane's eight consecutive elements as they lie in memory: 16 bytes of 16-bit values, 32 of fp32. With FULL all eight
 // are there; without, the first `cnt`, and the rest are zero.
 struct Raw8 {
@@ -385,15 +394,17 @@ __device__ __forceinline__ void step_block(const Block<CODED> &in, float sm, flo
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) g[e] = mul2(g[e], now.factor);
+    const pair_t zero = pair_of(0.0f, 0.0f);
     if (a.clip > 0.0f) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
+            nan_sum = fma2(g[e], zero, nan_sum);     // what is not finite is reported although the clamp makes an infinity finite
             const float2 x = halves(g[e]);
-            g[e] = pair_of(fminf(fmaxf(x.x, -a.clip), a.clip), fminf(fmaxf(x.y, -a.clip), a.clip));
+            g[e] = pair_of(clamped(x.x, a.clip), clamped(x.y, a.clip));
         }
     }
     const float wd = __fmul_rn(d.decay, __fmul_rn(a.lr, a.wd));
-    const pair_t minus_wd = pair_of(-wd, -wd), zero = pair_of(0.0f, 0.0f);
+    const pair_t minus_wd = pair_of(-wd, -wd);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         m[e] = add2(mul2(m[e], a.beta1), mul2(g[e], a.omb1));
