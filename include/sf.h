@@ -405,7 +405,7 @@ int sf_masked_dw_phase(const sf_dw_problem *probs /* host [n] */, int n, void *w
  * one whose clip makes an infinite gradient finite.
  *
  * sf_grad_norm: out[0] = inv_scale * sqrt(sum of squares of every gradient of every tensor) (the squares
- * of eight elements summed in fp32, from there in fp64, in a fixed order), out[1] =
+ * of eight elements summed in fp32, or in fp64 where fp32 does not hold them, from there in fp64, in a fixed order), out[1] =
  * inv_scale * min(1, max_norm / (out[0] + 1e-6)), or inv_scale when max_norm <= 0; out[1] = 0 (and SF_STATUS_NONFINITE) when the norm is not finite.
  * inv_scale undoes a loss scale (1 for none). Only n, g and g_type of a tensor are read. ws:
  * sf_grad_norm_ws_bytes() bytes, 16-byte aligned, zeroed once by the caller; every call leaves it

@@ -511,8 +511,33 @@ __global__ void count_step_kernel(int32_t *step, const float *factor, uint32_t *
 // ws of the norm: [0] CTAs that have finished (int32, 0 between calls), then a double per CTA.
 constexpr size_t kNormHeader = 16;
 
+// This thread's elements' squares in fp64, in its order.
+template <int N>
+__device__ __forceinline__ double squares64(const DenseBatch<N> &b)
+{
+    double sum = 0.0;
+    for (int unit = blockIdx.x; unit < b.units; unit += gridDim.x) {
+        const int which = find_tensor(b, unit);
+        const DenseDesc &d = b.d[which];
+        Place w(d, unit - b.unit_begin[which], b.per);
+        for (; w.more > 0; w.next()) {
+            pair_t g[4];
+            to_pairs(g, load_raw<false>(d.g, d.g_type, w.at, w.count()), d.g_type);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 x = halves(g[e]);
+                sum = fma((double)x.x, (double)x.x, sum);
+                sum = fma((double)x.y, (double)x.y, sum);
+            }
+        }
+    }
+    return sum;
+}
+
 // Sum of squares: fp32 over a lane's eight elements, fp64 from there. Every CTA leaves its sum in its own
-// place; the last one of the call adds them in a fixed order.
+// place; the last one of the call adds them in a fixed order. Where fp32 does not hold the squares (a thread's sum is not finite,
+// or so small that squares of its elements may have been lost, and not all of them are zero), the thread sums its elements
+// again in fp64. (2^26 x 3.1 bf16 elements: 74.5 us, 73.2 without the care, 77.7 with a check at each eight elements.)
 template <int N>
 __global__ void __launch_bounds__(kThreads)
 grad_norm_kernel(const __grid_constant__ DenseBatch<N> b, int32_t *done, double *sums, int at0, int total_ctas,
@@ -522,6 +547,7 @@ grad_norm_kernel(const __grid_constant__ DenseBatch<N> b, int32_t *done, double 
     __shared__ int is_last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     double sum = 0.0;
+    uint32_t any = 0;                                // a bit of some element
     griddep_wait();                                  // what the launches before this one wrote is there from here on
     for (int unit = blockIdx.x; unit < b.units; unit += gridDim.x) {
         const int which = find_tensor(b, unit);
@@ -537,6 +563,7 @@ grad_norm_kernel(const __grid_constant__ DenseBatch<N> b, int32_t *done, double 
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
+                any |= r[q].a.x | r[q].a.y | r[q].a.z | r[q].a.w | r[q].b.x | r[q].b.y | r[q].b.z | r[q].b.w;
                 pair_t g[4], s = pair_of(0.0f, 0.0f);
                 to_pairs(g, r[q], d.g_type);
 #pragma unroll
@@ -546,6 +573,7 @@ grad_norm_kernel(const __grid_constant__ DenseBatch<N> b, int32_t *done, double 
             }
         }
     }
+    if (any && !(sum >= 0x1p-80 && sum <= 0x1p1000)) sum = squares64(b);
     griddep_launch_dependents();                     // the launch behind this one may take what room is left
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);

@@ -51,3 +51,46 @@ def test_a_clip_through_the_plan_without_a_norm(sf, factor):
     plan, status = DensePlan([d], sf.AdamParams(lr=1e-2, clip=1e-3 * factor)), sf.status_word()
     plan.step(status)
     assert int(status) == sf.SF_STATUS_NONFINITE and bool(d.p[7].isnan()) and int(d.p.isnan().sum()) == 1
+
+
+@pytest.mark.parametrize("g_dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [1e25, 3e19, 1e-19, 1e-25, 1e-38])
+@pytest.mark.parametrize("n", [1, 8, 300, 70001])
+def test_the_norm_of_values_whose_squares_leave_fp32(sf, n, size, g_dt):
+    """Alone, and among values of ordinary size. Eight squares to a sum: 8 roundings, which the root halves, and those of
+    the result."""
+    gen = torch.Generator(device=DEV).manual_seed(n)
+    g = (torch.randn(n, generator=gen, device=DEV).double() * size).to(g_dt)
+    mixed = (torch.randn(n, generator=gen, device=DEV) * torch.where(torch.arange(n, device=DEV) % 3 == 0, size, 1.0)).to(g_dt)
+    zeros = torch.zeros(n, dtype=g_dt, device=DEV)
+    zeros[-1] = -0.0
+    for tensors in ([g], [mixed], [zeros, g, zeros]):
+        ds = [sf.Dense(torch.zeros(x.numel(), device=DEV), x) for x in tensors]
+        ts, out, status = sf.DenseTensors(ds), torch.zeros(2, device=DEV), sf.status_word()
+        sf.sf_grad_norm(ts, out, sf.grad_norm_workspace(ts), max_norm=1.0, inv_scale=0.5, status=status)
+        want = 0.5 * math.sqrt(sum(float(x.double().square().sum()) for x in tensors))
+        assert want < 3e38
+        # below 2^-126 the result itself is a multiple of 2^-149
+        assert abs(float(out[0]) - want) <= 6 * EPS32 * want + 2.0 ** -150
+        f = 0.5 * min(1.0, 1.0 / (want + 1e-6))
+        assert abs(float(out[1]) - f) <= 10 * EPS32 * f + 2.0 ** -150 and int(status) == 0
+
+
+@pytest.mark.parametrize("n", [1, 300])
+def test_a_norm_beyond_fp32_skips_the_step(sf, n):
+    ds = [sf.Dense(torch.ones(n, device=DEV), torch.full((n,), 3e38, device=DEV)) for _ in range(2)]
+    ts, out, status, step = sf.DenseTensors(ds), torch.zeros(2, device=DEV), sf.status_word(), sf.step_words()
+    sf.sf_grad_norm(ts, out, sf.grad_norm_workspace(ts), max_norm=1.0, status=status)
+    sf.sf_adamw_step(ts, sf.AdamParams(), step, out)
+    assert out.tolist() == [INF, 0.0] and int(status) == sf.SF_STATUS_NONFINITE and step.tolist() == [0, 0]
+    assert all(bool((d.p == 1).all()) for d in ds)
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_a_bad_value_in_the_norm(sf, bad):
+    """Beside values that take the fp64 sums."""
+    d = sf.Dense(torch.ones(300, device=DEV), torch.full((300,), 1e25, device=DEV))
+    d.g[290] = bad
+    ts, out, status = sf.DenseTensors([d]), torch.zeros(2, device=DEV), sf.status_word()
+    sf.sf_grad_norm(ts, out, sf.grad_norm_workspace(ts), max_norm=1.0, status=status)
+    assert not math.isfinite(float(out[0])) and float(out[1]) == 0.0 and int(status) == sf.SF_STATUS_NONFINITE
