@@ -375,7 +375,7 @@ struct StepNow {
 };
 
 // One block's step on what was loaded: this lane's eight elements. FULL: the block has all its 256.
-template <bool CODED, bool FULL>
+template <bool CODED, bool CLIP, bool FULL>
 __device__ __forceinline__ void step_block(const Block<CODED> &in, float sm, float sv, const DenseDesc &d, int64_t at, int64_t blk, int cnt,
                                            const StepArgs &a, const StepNow &now, pair_t &nan_sum)
 {
@@ -395,7 +395,7 @@ __device__ __forceinline__ void step_block(const Block<CODED> &in, float sm, flo
 #pragma unroll
     for (int e = 0; e < 4; ++e) g[e] = mul2(g[e], now.factor);
     const pair_t zero = pair_of(0.0f, 0.0f);
-    if (a.clip > 0.0f) {
+    if (CLIP) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             nan_sum = fma2(g[e], zero, nan_sum);     // what is not finite is reported although the clamp makes an infinity finite
@@ -440,7 +440,9 @@ __device__ __forceinline__ void step_block(const Block<CODED> &in, float sm, flo
 // waits: a block is loaded where it is used, its lines are asked for in L2 one block ahead, and the scales, which those
 // lines leave out, are fetched for the whole unit at its beginning (2^26 elements over fp32 weights: 176 us, 203 with the
 // scales loaded block by block, 6.1 TB/s against 5.3).
-template <int N, bool CODED>
+// CLIP: an element clip is on. It has instances of its own, so that steps without one do not pay for its registers (a 7B-shaped
+// layer with fp32 moments 846 us; 852 with both in one).
+template <int N, bool CODED, bool CLIP>
 __global__ void __launch_bounds__(kThreads, CODED ? 4 : 3)
 adamw_kernel(const __grid_constant__ DenseBatch<N> b, const __grid_constant__ StepArgs a, uint32_t *status)
 {
@@ -480,8 +482,8 @@ adamw_kernel(const __grid_constant__ DenseBatch<N> b, const __grid_constant__ St
         }
         w.next();
         const float sm = CODED ? __shfl_sync(0xffffffffu, sms, k) : 0.0f, sv = CODED ? __shfl_sync(0xffffffffu, svs, k) : 0.0f;
-        if (full) step_block<CODED, true>(in, sm, sv, d, at, blk, 8, a, now, nan_sum);
-        else step_block<CODED, false>(in, sm, sv, d, at, blk, cnt, a, now, nan_sum);
+        if (full) step_block<CODED, CLIP, true>(in, sm, sv, d, at, blk, 8, a, now, nan_sum);
+        else step_block<CODED, CLIP, false>(in, sm, sv, d, at, blk, cnt, a, now, nan_sum);
         if (!CODED && w.more > 0) in.load(d, w);
     }
     griddep_launch_dependents();                     // the launch behind this one may take what room is left
@@ -757,7 +759,7 @@ int launch_step(const sf_dense *t, int n, int per, bool last, StepArgs a, uint32
         a.last = last && li == launches - 1;
         // a CTA to a unit: dealt out as SMs come free (a 7B-shaped layer with 8-bit moments, when this was chosen: 518 us
         // against 588 with eight CTAs to an SM that took units in turn)
-        const int rc = launch_early(adamw_kernel<N, CODED>, (int)units, stream, b, a, status);
+        const int rc = launch_early(a.clip > 0.0f ? adamw_kernel<N, CODED, true> : adamw_kernel<N, CODED, false>, (int)units, stream, b, a, status);
         if (rc != SF_OK) return rc;
     }
     return SF_OK;
