@@ -109,7 +109,8 @@ __device__ __forceinline__ int find_tensor(const DenseBatch<N> &b, int unit)
 // residual r r - x is exact in one fused operation, and r - (r r - x) y / 2 is the root to the last place (tests hold it
 // to the correctly rounded one). The library's root, with its paths for numbers outside the normal ones, took a third of
 // the step's instructions. Zero gives zero. The residual is a multiple of 2^-149, so it is off by up to 2^-150 and the
-// root by up to 2^-150 y / 2, which is 2^-151 / x of it: nothing down to 2^-100, a quarter of a step at 2^-126.
+// root by up to 2^-150 y / 2, which is 2^-151 / x of it: nothing down to 2^-100, a quarter of a step at 2^-126. An infinite x,
+// whose residual is not a number, gives infinity (a NaN does too: its moment and weight are NaN without the root).
 __device__ __forceinline__ pair_t root2_of(pair_t x)
 {
     const float2 v = halves(x);
@@ -118,7 +119,8 @@ __device__ __forceinline__ pair_t root2_of(pair_t x)
     asm("rsqrt.approx.f32 %0, %1;" : "=f"(yb) : "f"(fmaxf(v.y, 0x1p-149f)));
     const pair_t y = pair_of(ya, yb), r = mul2(x, y);
     const pair_t off = fma2(r, r, mul2(x, pair_of(-1.0f, -1.0f)));
-    return fma2(off, mul2(y, pair_of(-0.5f, -0.5f)), r);
+    const float2 root = halves(fma2(off, mul2(y, pair_of(-0.5f, -0.5f)), r));
+    return pair_of(fminf(root.x, __int_as_float(0x7f800000)), fminf(root.y, __int_as_float(0x7f800000)));
 }
 
 // a / b within 2 units in the last place for the sizes that occur here (b normal, below 2^126).

@@ -94,3 +94,24 @@ def test_a_bad_value_in_the_norm(sf, bad):
     ts, out, status = sf.DenseTensors([d]), torch.zeros(2, device=DEV), sf.status_word()
     sf.sf_grad_norm(ts, out, sf.grad_norm_workspace(ts), max_norm=1.0, status=status)
     assert not math.isfinite(float(out[0])) and float(out[1]) == 0.0 and int(status) == sf.SF_STATUS_NONFINITE
+
+
+@pytest.mark.parametrize("p_dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("state8", [False, True])
+@pytest.mark.parametrize("at", [5, 290])
+@pytest.mark.parametrize("size", [1e20, -3e30])
+def test_a_square_beyond_fp32_leaves_the_weight_finite(sf, size, at, state8, p_dt):
+    """The root moment becomes infinite and the update m / v zero: the weight decays and no more, as the formula has it. The
+    moment is reported. One step: 4 roundings of p, 40 of an update of lr, and half a step of the weights' type."""
+    hp = sf.AdamParams(lr=1e-2, wd=0.1)
+    d = make(sf, 300, p_dt, torch.float32, sf.SF_TYPE_E4M3 if state8 else sf.SF_TYPE_F32, True, 3)
+    d.g[at] = size
+    status, before = sf.status_word(), d.p.double().clone()
+    ref = Ref(d.p, d.m.float(), d.v.float())
+    ref.step(d.g, 1, hp, 1.0)
+    ref.p[at] = float(before[at]) * (1 - float(np.float32(hp.lr)) * float(np.float32(hp.wd)))
+    sf.sf_adamw_step(sf.DenseTensors([d]), hp, sf.step_words(), status=status)
+    assert int(status) == sf.SF_STATUS_NONFINITE and bool(d.p.isfinite().all()) and bool(d.live.isfinite().all())
+    tol = (4 * EPS32 + half_step(p_dt)) * np.abs(ref.p) + 40 * EPS32 * hp.lr
+    assert np.all(np.abs(d.p.double().cpu().numpy() - ref.p) <= tol)
+    assert int((~(d.v_scale if state8 else d.v).isfinite()).sum()) == 1
