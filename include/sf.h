@@ -462,10 +462,12 @@ int sf_adamw_step(const sf_dense *t /* host [n] */, int n, const sf_adam *hp, in
  * set. Pipeline waits are bounded as in sf_masked_dw (SF_STATUS_WAIT_TIMEOUT).
  * Deterministic: every result is summed in an order that the sizes and, for the weight gradient, the
  * expert's tokens give; which rows share a tile changes no sum. The written operand
- * must not overlap the others (one address for two operands is refused). Requirements: 1 <= E <= 1024; T >= 0; R, C positive multiples of 8;
+ * must not overlap the others (one address for two operands is refused). Requirements: 1 <= E <= 1024; 0 <= T <= 2^30;
+ * R, C positive multiples of 8, at most 2^30;
  * ld_a >= C, ld_y >= R, ld_w >= C, stride_w >= (R - 1) * ld_w + C when E > 1; strides multiples of 8 elements
  * (4 for an fp32 W); A, W, Y 16-byte aligned (A and Y may be NULL when T = 0). One launch a call.
- * Errors: SF_ERR_ARG, SF_ERR_ALIGN, SF_ERR_UNSUPPORTED (E above 1024, or more than 2^30 tiles).
+ * Errors: SF_ERR_ARG, SF_ERR_ALIGN, SF_ERR_UNSUPPORTED (E above 1024; T, R or C above 2^30; a stride above 2^38; or work in more
+ * than 2^30 pieces, counted as (T / 16 + E) * (max(R, C) / 128 + 1), or as E * (R / 256) * (C / 64) rounded up).
  */
 #define SF_GROUPED_MAX_EXPERTS 1024
 

@@ -613,8 +613,8 @@ def grouped_problem(A, W, Y, offsets) -> Desc:
     (T, C), (E, R) = A.shape, W.shape[:2]
     if W.shape[2] != C or tuple(Y.shape) != (T, R):
         raise ValueError(f"shapes do not match: A {tuple(A.shape)}, W {tuple(W.shape)}, Y {tuple(Y.shape)}")
-    if max(E, T, R, C) >= 2 ** 31:
-        raise ValueError("sizes are 32-bit")
+    if E >= 2 ** 31 or max(T, R, C) > 2 ** 30:
+        raise ValueError("sizes are 32-bit: at most 2^30 tokens, rows and columns")
     for name, t in (("A", A), ("W", W), ("Y", Y)):
         if t.numel() and t.stride(-1) != 1:
             raise ValueError(f"{name}: columns must be contiguous")

@@ -281,7 +281,7 @@ __device__ __forceinline__ int accumulator_of(const PUnit &x, int &turn)
 // The tile size for these offsets: the one whose rounds of units, at the mean cost of a unit, end first. A unit's time
 // is about that of its accumulator columns and 128 more, for its weights and its ends (measured, 4 rounds of 4,096-long
 // sums: 154, 204 and 248 us at 256, 384 and 512 tokens), so large tiles win unless they leave the last round empty.
-// A warp to a candidate, a lane to an expert; every thread gets the answer. Contains __syncthreads.
+// Counted in steps of 32 columns. A warp to a candidate, a lane to an expert; every thread gets the answer. Contains __syncthreads.
 __device__ __forceinline__ int choose_tile(Plan &pl, const GArgs &g, int workers)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -293,7 +293,7 @@ __device__ __forceinline__ int choose_tile(Plan &pl, const GArgs &g, int workers
             if (cnt == 0) continue;
             const int tile = tile_tokens(cnt, most, 32), n = quot_up(cnt, tile);
             tiles += n;
-            cost += (n - 1) * (tile + 128) + ((cnt - (n - 1) * tile + 31) & ~31) + 128;
+            cost += (n - 1) * (tile / 32 + 4) + (cnt - (n - 1) * tile + 31) / 32 + 4;
         }
         tiles = __reduce_add_sync(0xffffffffu, tiles);
         cost = __reduce_add_sync(0xffffffffu, cost);
@@ -1640,6 +1640,9 @@ int check_grouped(const sf_grouped *p, bool dw)
         if (!aligned16(p->A) || !aligned16(p->Y) || (p->ld_a & 7) || (p->ld_y & 7)) return SF_ERR_ALIGN;
     }
     if (p->E > kMaxE) return SF_ERR_UNSUPPORTED;
+    // The kernels round counts up to whole tiles, and add numbers of tiles to them, in 32 bits.
+    const int most = 1 << 30;
+    if (p->T > most || p->R > most || p->C > most) return SF_ERR_UNSUPPORTED;
     // byte strides a tensor map can hold (below 2^40), and tile counts that stay far inside 32 bits
     const int64_t far = (int64_t)1 << 38;
     if (p->ld_w > far || p->stride_w > far || p->ld_a > far || p->ld_y > far) return SF_ERR_UNSUPPORTED;
@@ -1761,7 +1764,7 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
     // A token box that holds most experts in one tile: up to 32 tokens, where the weights outweigh the box, twice the
     // average (a decode batch of 12 tokens each: 114.6 us against 116.5 with a box of 16), beyond that the average and
     // a quarter (49 tokens each: 26.7 us with a box of 64, 31.0 with 128).
-    const int avg = (p->T + p->E - 1) / p->E;
+    const int64_t avg = ((int64_t)p->T + p->E - 1) / p->E;
     int nb = 16;
     while (nb < 128 && nb < p->T && 4 * nb < (nb < 32 ? 8 * avg : 5 * avg)) nb *= 2;
     const int64_t busy = p->E < p->T ? p->E : p->T;      // experts with a token, at most
