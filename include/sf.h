@@ -53,7 +53,8 @@ extern "C" {
 #define SF_STATUS_WAIT_TIMEOUT   0x8u  /* a kernel gave up a bounded wait and skipped its work */
 #define SF_STATUS_BAD_OFFSET     0x10u /* expert offsets fall or leave [0, T]: nothing was computed */
 /* Test hook: with SF_TEST_DW_WITHHOLD=1 in the environment, sf_masked_dw's first launch withholds
- * one pipeline stage of CTA 0, so that a bounded wait runs out and WAIT_TIMEOUT is raised. */
+ * one pipeline stage of CTA 0, so that a bounded wait runs out and WAIT_TIMEOUT is raised. With
+ * SF_TEST_GROUPED_WITHHOLD=1 the first stage of the sf_grouped_* calls' CTA 0 never completes. */
 
 typedef void *sf_stream;               /* cudaStream_t */
 
@@ -459,7 +460,8 @@ int sf_adamw_step(const sf_dense *t /* host [n] */, int n, const sf_adam *hp, in
  * added to what W holds, and an expert without tokens keeps it. A non-finite value reaches only the
  * results whose sums hold it.
  * offsets must not fall and must lie in [0, T]: otherwise nothing is computed and SF_STATUS_BAD_OFFSET is
- * set. Pipeline waits are bounded as in sf_masked_dw (SF_STATUS_WAIT_TIMEOUT).
+ * set. Pipeline waits are bounded as in sf_masked_dw (SF_STATUS_WAIT_TIMEOUT): a CTA,
+ * pair or cluster of CTAs that gives up stores nothing more.
  * Deterministic: every result is summed in an order that the sizes and, for the weight gradient, the
  * expert's tokens give; which rows share a tile changes no sum. The written operand
  * must not overlap the others (one address for two operands is refused). Requirements: 1 <= E <= 1024; 0 <= T <= 2^30;

@@ -217,6 +217,18 @@ SF_DEVICE float2 ld_cluster_f32x2(uint32_t addr, int rank)
     return v;
 }
 
+// The same for one 32-bit word.
+SF_DEVICE int ld_cluster_s32(uint32_t addr, int rank)
+{
+    int v;
+    asm volatile(
+        "{\n\t.reg .b32 ra;\n\t"
+        "mapa.shared::cluster.u32 ra, %1, %2;\n\t"
+        "ld.shared::cluster.s32 %0, [ra];\n\t}"
+        : "=r"(v) : "r"(addr), "r"(rank) : "memory");
+    return v;
+}
+
 // 2-D tiled TMA load by either CTA of a pair into its own shared memory, completing its bytes on
 // the mbarrier at `bar`'s offset in the even CTA (the one whose thread issues the pair's MMAs).
 // No multicast.
