@@ -494,6 +494,23 @@ int sf_grouped_forward(const sf_grouped *p /* host */, uint32_t *dev_status, sf_
 int sf_grouped_dx(const sf_grouped *p /* host */, uint32_t *dev_status, sf_stream stream);
 int sf_grouped_dw(const sf_grouped *p /* host */, int accumulate, uint32_t *dev_status, sf_stream stream);
 
+/* Which kernel a call with these sizes takes on the current device, without making it: for tests and measurements. A negative
+ * value is the call's error. Nothing is read on the device; the addresses are checked only. */
+#define SF_GROUPED_FORWARD 0
+#define SF_GROUPED_DX      1
+#define SF_GROUPED_DW      2
+
+#define SF_GROUPED_NONE      0   /* no tokens: nothing is launched */
+#define SF_GROUPED_SINGLE    1   /* single CTAs, a unit each */
+#define SF_GROUPED_ROUNDS    2   /* single CTAs, several units each */
+#define SF_GROUPED_SLICES    3   /* single CTAs, the sums in slices within each */
+#define SF_GROUPED_CLUSTERS  4   /* and over the CTAs of a cluster */
+#define SF_GROUPED_PAIRS     5   /* CTA pairs */
+#define SF_GROUPED_PAIRS_FEW 6   /* weight gradient: CTA pairs, few tokens to an expert */
+#define SF_GROUPED_PAIRS_ADD 7   /* weight gradient: the same, added to in shared memory */
+
+int sf_grouped_kernel(const sf_grouped *p /* host */, int product, int accumulate);
+
 /* ---- helpers (not on the hot path) ------------------------------------------------------ */
 
 /* Quantise a full-precision matrix into the int8 + scale + residual storage of section 2.3

@@ -40,6 +40,15 @@ SF_TYPE_E4M3 = 3
 SF_DENSE_BLOCK = 256
 SF_DENSE_PER_LAUNCH = 384
 SF_GROUPED_MAX_EXPERTS = 1024
+SF_GROUPED_FORWARD, SF_GROUPED_DX, SF_GROUPED_DW = 0, 1, 2
+SF_GROUPED_NONE = 0
+SF_GROUPED_SINGLE = 1
+SF_GROUPED_ROUNDS = 2
+SF_GROUPED_SLICES = 3
+SF_GROUPED_CLUSTERS = 4
+SF_GROUPED_PAIRS = 5
+SF_GROUPED_PAIRS_FEW = 6
+SF_GROUPED_PAIRS_ADD = 7
 
 SF_DW_MAX_PER_LAUNCH = 96
 SF_MASKS_PER_LAUNCH = 240
@@ -148,7 +157,8 @@ def load():
     L.sf_grouped_forward.argtypes = [ctypes.POINTER(sf_grouped), _P, _P]
     L.sf_grouped_dx.argtypes = [ctypes.POINTER(sf_grouped), _P, _P]
     L.sf_grouped_dw.argtypes = [ctypes.POINTER(sf_grouped), ctypes.c_int, _P, _P]
-    for name in ("sf_grad_norm", "sf_adamw_step", "sf_grouped_forward", "sf_grouped_dx", "sf_grouped_dw"):
+    L.sf_grouped_kernel.argtypes = [ctypes.POINTER(sf_grouped), ctypes.c_int, ctypes.c_int]
+    for name in ("sf_grad_norm", "sf_adamw_step", "sf_grouped_forward", "sf_grouped_dx", "sf_grouped_dw", "sf_grouped_kernel"):
         getattr(L, name).restype = ctypes.c_int
     for name in ("sf_mask_init", "sf_mask_update", "sf_masked_dw", "sf_embed_grad", "sf_adam_tables",
                  "sf_sparse_update", "sf_quantize_init", "sf_mask_update_phase", "sf_masked_dw_phase",
@@ -654,3 +664,12 @@ def sf_grouped_dw(p: Desc, status=None, stream=None, accumulate: bool = False):
     """W[e] = sum over e's tokens of Y[t] A[t]^T: the weight gradient, with Y the gradient of the outputs;
     accumulate adds it to what W (fp32) holds."""
     _grouped("sf_grouped_dw", p, status, stream, int(accumulate))
+
+
+def sf_grouped_kernel(p: Desc, product: int, accumulate: bool = False) -> int:
+    """Which kernel (SF_GROUPED_SINGLE ..) the call takes on the current device: for tests and measurements."""
+    _on_current(_one_device(p.refs[1]))
+    k = load().sf_grouped_kernel(ctypes.byref(p.c), product, int(accumulate))
+    if k < 0:
+        _check(k, "sf_grouped_kernel")
+    return k

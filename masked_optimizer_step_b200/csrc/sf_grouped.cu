@@ -1814,6 +1814,95 @@ constexpr int64_t kDwOldBelow = 512;
 // 140 / 147, 159 / 154 and 254 / 209 us for 4 of 11008 x 4096.
 constexpr int64_t kDwFewBelow = 128;
 
+// What a call takes.
+struct Choice {
+    int kernel;                // SF_GROUPED_*
+    int slices, split;         // single CTAs: slices of the sums in a CTA, CTAs (a cluster) that share a unit's
+    int nb, stages;            // single CTAs: token box (forward, dx), stages
+    int64_t units;             // at most
+};
+
+Choice choose_product(const sf_grouped *p, bool fwd, int sms)
+{
+    Choice x = {};
+    const int M = fwd ? p->R : p->C, nk = ((fwd ? p->C : p->R) + GK - 1) / GK;
+    // A token box that holds most experts in one tile: up to 32 tokens, where the weights outweigh the box, twice the
+    // average (a decode batch of 12 tokens each: 114.6 us against 116.5 with a box of 16), beyond that the average and
+    // a quarter (49 tokens each: 26.7 us with a box of 64, 31.0 with 128).
+    const int64_t avg = ((int64_t)p->T + p->E - 1) / p->E;
+    int nb = 16;
+    while (nb < 128 && nb < p->T && 4 * nb < (nb < 32 ? 8 * avg : 5 * avg)) nb *= 2;
+    const int64_t busy = p->E < p->T ? p->E : p->T;      // experts with a token, at most
+    const int64_t tiles = busy + p->T / nb;              // token tiles, at most
+    const int64_t m_tiles = (M + SM_ROWS - 1) / SM_ROWS;
+    const bool one_round = tiles * m_tiles <= 2 * sms;
+
+    if (!one_round && p->T > pair_from(nk) * p->E) {
+        x.kernel = SF_GROUPED_PAIRS;
+        x.units = ((int64_t)p->T / 64 + p->E) * ((M + PM - 1) / PM);
+        return x;
+    }
+    // K in slices while the units fit the device at once, two CTAs to an SM, with a token tile to an expert where most experts'
+    // tokens fit one. Where they take several, only long sums that leave half of the SMs without work (one expert of 64 x 4096
+    // over 300, 1,000 and 8,000 tokens: 23.8, 24.4 and 25.2 us without slices, 8.4, 9.2 and 15.3 with; 3 of 88 x 560 over 416
+    // each 8.9 / 9.5, one of 184 x 9632 over 7,202 53 / 69).
+    const bool one_tile = avg <= nb;
+    int s = 1;
+    while (s < 4 && (one_tile ? busy * m_tiles <= sms / s : tiles * m_tiles <= sms / (2 * s)) && nk >= (one_tile ? 4 : 10) * s && 2 * s * nb <= 256)
+        s *= 2;
+    // Several units to a CTA, planned ahead, where a unit is short (64 experts of 1024 x 1024 over 64 tokens each: 35.6 ->
+    // 32.1 us); long ones come out more even as a CTA each (the decode batch above: 114.6 against 117.5 us).
+    const bool rounds = s == 1 && tiles * m_tiles > 2 * sms && nk <= 24;
+    const int stage_bytes = S_W_BYTES + s * nb * GK * 2;
+    const int rows = SM_ROWS / s;
+    x.units = tiles * ((M + rows - 1) / rows);
+    // The slices over the CTAs of a cluster, too, while the units still fit and a CTA keeps two steps or more (alone against
+    // in clusters: one expert of 64 x 4096 over 16 tokens 10.7 / 5.0 us, 512 x 11008 over 100 tokens 45.3 / 11.4, 4096 x 4096
+    // over 2 tokens 11.0 / 8.9; with a step a CTA, 2 experts of 512 x 512 over 2 tokens each, 4.0 / 4.7).
+    x.split = 1;
+    while (s > 1 && x.split < 8 && x.units * 2 * x.split <= sms * 7 / 4 && nk >= 2 * 2 * x.split * s) x.split *= 2;
+    // One CTA to an SM, or two. Clusters do not fill every SM (8 experts of 128 x 2048 over 2 tokens each, 144 CTAs in
+    // clusters of 4: 7.9 us with one to an SM, 5.3 with two).
+    x.stages = (x.units * x.split <= (x.split > 1 ? sms * 3 / 4 : sms) ? S_RING_BYTES : S_RING_BYTES / 2) / stage_bytes;
+    if (x.stages > S_MAX_STAGES) x.stages = S_MAX_STAGES;
+    x.nb = nb;
+    x.slices = s;
+    x.kernel = rounds ? SF_GROUPED_ROUNDS : x.split > 1 ? SF_GROUPED_CLUSTERS : s > 1 ? SF_GROUPED_SLICES : SF_GROUPED_SINGLE;
+    return x;
+}
+
+Choice choose_dw(const sf_grouped *p, bool accumulate, int sms)
+{
+    Choice x = {};
+    auto tiles = [&](int rows, int cols) {
+        return (int64_t)((p->R + rows - 1) / rows) * ((p->C + cols - 1) / cols);
+    };
+    const int64_t busy = p->E < p->T ? p->E : p->T;      // experts with a token, at most
+    // Pairs, unless they would be few, or one round of single CTAs does it all with short sums (8 experts of 1024 x 1024
+    // over 128 tokens each: 11.1 us against 13.1; one of 2048 x 2048 over 4,096: 56 us against 30).
+    const bool one_round = busy * tiles(SM_ROWS, PN) <= 2 * sms && p->T <= (int64_t)512 * p->E;
+    if (busy * tiles(PM, PN) >= sms / 4 && !one_round) {
+        const bool few = p->T < (accumulate ? kDwOldBelow : kDwFewBelow) * p->E;
+        x.kernel = !few ? SF_GROUPED_PAIRS : accumulate ? SF_GROUPED_PAIRS_ADD : SF_GROUPED_PAIRS_FEW;
+        x.units = p->E * tiles(PM, PN);
+        return x;
+    }
+    // Tokens in slices while the units still fit the device at once (one expert of 512 x 512 over 8,192 tokens: 102, 43 and
+    // 24 us with 1, 2 and 4 slices; where they do not fit, every slice more costs its share of the loads again).
+    int s = 1;
+    while (s < 4 && busy * tiles(SM_ROWS / (2 * s), PN / (2 * s)) <= 2 * sms && p->T > (int64_t)GK * s * p->E) s *= 2;
+    x.slices = s;
+    // Four slices in each CTA of a cluster while the CTAs fit one to an SM and keep more than four steps (alone against in
+    // clusters: one expert of 128 x 128 over 65,536 tokens 151 / 31 us, of 64 x 512 over 8,192 tokens 22.3 / 9.5; with
+    // shorter sums or fewer slices clusters cost what they save).
+    x.split = 1;
+    x.units = p->E * tiles(SM_ROWS / s, PN / s);
+    while (s == 4 && x.split < 8 && x.units * 2 * x.split <= sms && p->T > (int64_t)4 * GK * 4 * 2 * x.split * p->E) x.split *= 2;
+    x.stages = x.units * x.split <= (x.split > 1 ? sms * 3 / 4 : sms) ? D_MAX_STAGES : D_MAX_STAGES / 2;       // one CTA to an SM, or two
+    x.kernel = x.split > 1 ? SF_GROUPED_CLUSTERS : s > 1 ? SF_GROUPED_SLICES : SF_GROUPED_SINGLE;
+    return x;
+}
+
 template <bool TRANS>
 int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
 {
@@ -1837,66 +1926,34 @@ int grouped_product(const sf_grouped *p, uint32_t *status, sf_stream stream)
     const void *x = fwd ? p->A : p->Y;
     const int64_t ld_x = fwd ? p->ld_a : p->ld_y;
     const int64_t stride = p->E > 1 ? p->stride_w : (int64_t)p->R * p->ld_w;
-    const int w_rows = fwd ? 128 : 64;
-    const int nk = (g.K + GK - 1) / GK;
+    const Choice c = choose_product(p, fwd, sms);
 
-    // A token box that holds most experts in one tile: up to 32 tokens, where the weights outweigh the box, twice the
-    // average (a decode batch of 12 tokens each: 114.6 us against 116.5 with a box of 16), beyond that the average and
-    // a quarter (49 tokens each: 26.7 us with a box of 64, 31.0 with 128).
-    const int64_t avg = ((int64_t)p->T + p->E - 1) / p->E;
-    int nb = 16;
-    while (nb < 128 && nb < p->T && 4 * nb < (nb < 32 ? 8 * avg : 5 * avg)) nb *= 2;
-    const int64_t busy = p->E < p->T ? p->E : p->T;      // experts with a token, at most
-    const int64_t tiles = busy + p->T / nb;              // token tiles, at most
-    const int64_t m_tiles = (g.M + SM_ROWS - 1) / SM_ROWS;
-    const bool one_round = tiles * m_tiles <= 2 * sms;
-
-    if (!one_round && p->T > pair_from(nk) * p->E) {
+    if (c.kernel == SF_GROUPED_PAIRS) {
         if (!prepare_kernel(grouped_pair_kernel<TRANS>, T_SMEM_BYTES)) return SF_ERR_CUDA;
-        if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, w_rows) ||
+        if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, fwd ? 128 : 64) ||
             !encode(&g.tm_y, p->type, g.out, g.M, p->T, g.ld_out, 0, 0, 16, 256))
             return SF_ERR_CUDA;
         for (int b = 0; b < 4; ++b)
             if (!encode(&g.tm_t[b], p->type, x, g.K, p->T, ld_x, 0, 0, 32 * (b + 1))) return SF_ERR_CUDA;
         const int slots = pair_slots();
         if (slots <= 0) return SF_ERR_CUDA;
-        const int64_t most = ((int64_t)p->T / 64 + p->E) * ((g.M + PM - 1) / PM);
-        const int pairs = (int)(most < slots ? most : slots);
+        const int pairs = (int)(c.units < slots ? c.units : slots);
         return launch(grouped_pair_kernel<TRANS>, 2 * pairs, 2, P_THREADS, T_SMEM_BYTES, g, status, stream);
     }
-    // K in slices while the units fit the device at once, two CTAs to an SM, with a token tile to an expert where most experts'
-    // tokens fit one. Where they take several, only long sums that leave half of the SMs without work (one expert of 64 x 4096
-    // over 300, 1,000 and 8,000 tokens: 23.8, 24.4 and 25.2 us without slices, 8.4, 9.2 and 15.3 with; 3 of 88 x 560 over 416
-    // each 8.9 / 9.5, one of 184 x 9632 over 7,202 53 / 69).
-    const bool one_tile = avg <= nb;
-    int s = 1;
-    while (s < 4 && (one_tile ? busy * m_tiles <= sms / s : tiles * m_tiles <= sms / (2 * s)) && nk >= (one_tile ? 4 : 10) * s && 2 * s * nb <= 256)
-        s *= 2;
-    g.nb = nb;
-    // Several units to a CTA, planned ahead, where a unit is short (64 experts of 1024 x 1024 over 64 tokens each: 35.6 ->
-    // 32.1 us); long ones come out more even as a CTA each (the decode batch above: 114.6 against 117.5 us).
-    const bool rounds = s == 1 && tiles * m_tiles > 2 * sms && nk <= 24;
-    const int stage_bytes = S_W_BYTES + s * nb * GK * 2;
-    const int rows = SM_ROWS / s;
-    const int64_t units = tiles * ((g.M + rows - 1) / rows);                       // at most
-    // The slices over the CTAs of a cluster, too, while the units still fit and a CTA keeps two steps or more (alone against
-    // in clusters: one expert of 64 x 4096 over 16 tokens 10.7 / 5.0 us, 512 x 11008 over 100 tokens 45.3 / 11.4, 4096 x 4096
-    // over 2 tokens 11.0 / 8.9; with a step a CTA, 2 experts of 512 x 512 over 2 tokens each, 4.0 / 4.7).
-    g.split = 1;
-    while (s > 1 && g.split < 8 && units * 2 * g.split <= sms * 7 / 4 && nk >= 2 * 2 * g.split * s) g.split *= 2;
-    // One CTA to an SM, or two. Clusters do not fill every SM (8 experts of 128 x 2048 over 2 tokens each, 144 CTAs in
-    // clusters of 4: 7.9 us with one to an SM, 5.3 with two).
-    g.stages = (units * g.split <= (g.split > 1 ? sms * 3 / 4 : sms) ? S_RING_BYTES : S_RING_BYTES / 2) / stage_bytes;
-    if (g.stages > S_MAX_STAGES) g.stages = S_MAX_STAGES;
-    const int box_rows = fwd ? rows : 64, box_bytes = !fwd && s == 4 ? 64 : 128;
-    auto kernel = rounds ? grouped_small_kernel<TRANS, 1, true> : s == 1 ? grouped_small_kernel<TRANS, 1, false>
-                  : s == 2 ? grouped_small_kernel<TRANS, 2, false> : grouped_small_kernel<TRANS, 4, false>;
+    const bool rounds = c.kernel == SF_GROUPED_ROUNDS;
+    g.nb = c.nb;
+    g.split = c.split;
+    g.stages = c.stages;
+    auto kernel = rounds ? grouped_small_kernel<TRANS, 1, true> : c.slices == 1 ? grouped_small_kernel<TRANS, 1, false>
+                  : c.slices == 2 ? grouped_small_kernel<TRANS, 2, false> : grouped_small_kernel<TRANS, 4, false>;
     if (!prepare_kernel(kernel, S_SMEM_BYTES)) return SF_ERR_CUDA;
+    const int box_rows = fwd ? SM_ROWS / c.slices : 64, box_bytes = !fwd && c.slices == 4 ? 64 : 128;
     if (!encode(&g.tm_w, p->type, p->W, p->C, p->R, p->ld_w, p->E, stride, box_rows, box_bytes)) return SF_ERR_CUDA;
-    for (int b = 0; 16 << b <= nb; ++b)
+    for (int b = 0; 16 << b <= c.nb; ++b)
         if (!encode(&g.tm_t[b], p->type, x, g.K, p->T, ld_x, 0, 0, 16 << b)) return SF_ERR_CUDA;
-    const int grid = (int)(rounds ? 2 * sms : units * g.split);
-    return launch(kernel, grid, g.split, S_THREADS, (size_t)g.stages * stage_bytes + 1024, g, status, stream);
+    const int grid = (int)(rounds ? 2 * sms : c.units * c.split);
+    const size_t smem = (size_t)c.stages * (S_W_BYTES + c.slices * c.nb * GK * 2) + 1024;
+    return launch(kernel, grid, c.split, S_THREADS, smem, g, status, stream);
 }
 
 }  // namespace
@@ -1939,17 +1996,11 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
     const void *a = p->T > 0 ? p->A : p->W, *y = p->T > 0 ? p->Y : p->W;
     const int64_t ld_a = p->T > 0 ? p->ld_a : p->C, ld_y = p->T > 0 ? p->ld_y : p->R;
     const int64_t stride = p->E > 1 ? p->stride_w : (int64_t)p->R * p->ld_w;
-    auto tiles = [&](int rows, int cols) {
-        return (int64_t)((p->R + rows - 1) / rows) * ((p->C + cols - 1) / cols);
-    };
-    const int64_t busy = p->E < p->T ? p->E : p->T;      // experts with a token, at most
-    const int64_t pair_units = p->E * tiles(PM, PN);
-    // Pairs, unless they would be few, or one round of single CTAs does it all with short sums (8 experts of 1024 x 1024
-    // over 128 tokens each: 11.1 us against 13.1; one of 2048 x 2048 over 4,096: 56 us against 30).
-    const bool one_round = busy * tiles(SM_ROWS, PN) <= 2 * sms && p->T <= (int64_t)512 * p->E;
-    if (busy * tiles(PM, PN) >= sms / 4 && !one_round) {
-        const bool few = p->T < (accumulate ? kDwOldBelow : kDwFewBelow) * p->E;
-        auto kernel = !few ? grouped_dw_kernel<false, false> : accumulate ? grouped_dw_kernel<true, true> : grouped_dw_kernel<false, true>;
+    const Choice c = choose_dw(p, accumulate != 0, sms);
+    if (c.kernel >= SF_GROUPED_PAIRS) {
+        auto kernel = c.kernel == SF_GROUPED_PAIRS     ? grouped_dw_kernel<false, false>
+                      : c.kernel == SF_GROUPED_PAIRS_ADD ? grouped_dw_kernel<true, true>
+                                                         : grouped_dw_kernel<false, true>;
         if (!prepare_kernel(kernel, W_SMEM_BYTES)) return SF_ERR_CUDA;
         if (!encode(&g.tm_w, p->type, a, p->C, p->T, ld_a, 0, 0, 64) || !encode(&g.tm_x, p->type, y, p->R, p->T, ld_y, 0, 0, 64) ||
             !encode(&g.tm_out, p->w_type, p->W, p->C, p->R, p->ld_w, p->E, stride, 32))
@@ -1960,28 +2011,31 @@ extern "C" int sf_grouped_dw(const sf_grouped *p, int accumulate, uint32_t *dev_
         // 4096 over 1,024 tokens and more: 2% less).
         if (p->T > 0 && p->R % 64 == 0 && encode_chunks(&g.tm_t[0], p->type, y, p->R, p->T, ld_y, 2)) g.whole |= 1;
         if (p->T > 0 && p->C % 64 == 0 && encode_chunks(&g.tm_t[1], p->type, a, p->C, p->T, ld_a, 2)) g.whole |= 2;
-        return launch(kernel,
-                      2 * (int)(pair_units < slots ? pair_units : slots), 2, W_THREADS, W_SMEM_BYTES, g, dev_status, stream);
+        return launch(kernel, 2 * (int)(c.units < slots ? c.units : slots), 2, W_THREADS, W_SMEM_BYTES, g, dev_status, stream);
     }
-    // Tokens in slices while the units still fit the device at once (one expert of 512 x 512 over 8,192 tokens: 102, 43 and
-    // 24 us with 1, 2 and 4 slices; where they do not fit, every slice more costs its share of the loads again).
-    int s = 1;
-    while (s < 4 && busy * tiles(SM_ROWS / (2 * s), PN / (2 * s)) <= 2 * sms && p->T > (int64_t)GK * s * p->E) s *= 2;
-    g.split = 1;
-    // Four slices in each CTA of a cluster while the CTAs fit one to an SM and keep more than four steps (alone against in
-    // clusters: one expert of 128 x 128 over 65,536 tokens 151 / 31 us, of 64 x 512 over 8,192 tokens 22.3 / 9.5; with
-    // shorter sums or fewer slices clusters cost what they save).
-    const int64_t units = p->E * tiles(SM_ROWS / s, PN / s);
-    while (s == 4 && g.split < 8 && units * 2 * g.split <= sms && p->T > (int64_t)4 * GK * 4 * 2 * g.split * p->E) g.split *= 2;
-    g.stages = units * g.split <= (g.split > 1 ? sms * 3 / 4 : sms) ? D_MAX_STAGES : D_MAX_STAGES / 2;       // one CTA to an SM, or two
-    auto kernel = g.split > 1 ? grouped_dw_small_kernel<4, true> : s == 1 ? grouped_dw_small_kernel<1, false>
-                  : s == 2 ? grouped_dw_small_kernel<2, false> : grouped_dw_small_kernel<4, false>;
+    g.split = c.split;
+    g.stages = c.stages;
+    auto kernel = c.split > 1 ? grouped_dw_small_kernel<4, true> : c.slices == 1 ? grouped_dw_small_kernel<1, false>
+                  : c.slices == 2 ? grouped_dw_small_kernel<2, false> : grouped_dw_small_kernel<4, false>;
     if (!prepare_kernel(kernel, D_SMEM_BYTES)) return SF_ERR_CUDA;
     if (!encode(&g.tm_w, p->type, a, p->C, p->T, ld_a, 0, 0, 64) ||
-        !encode(&g.tm_x, p->type, y, p->R, p->T, ld_y, 0, 0, 64, s == 4 ? 64 : 128))
+        !encode(&g.tm_x, p->type, y, p->R, p->T, ld_y, 0, 0, 64, c.slices == 4 ? 64 : 128))
         return SF_ERR_CUDA;
     // 2 copies a stage in place of 6 (8 experts of 1024 x 1024 over 128 tokens each: 11.7 -> 10.4 us; with slices no gain)
-    if (p->T > 0 && s == 1 && p->R % 64 == 0 && encode_chunks(&g.tm_t[0], p->type, y, p->R, p->T, ld_y, 2)) g.whole |= 1;
-    if (p->T > 0 && s == 1 && p->C % 64 == 0 && encode_chunks(&g.tm_t[1], p->type, a, p->C, p->T, ld_a, 4)) g.whole |= 2;
-    return launch(kernel, (int)units * g.split, g.split, D_THREADS, (size_t)g.stages * D_STAGE_BYTES + 1024, g, dev_status, stream);
+    if (p->T > 0 && c.slices == 1 && p->R % 64 == 0 && encode_chunks(&g.tm_t[0], p->type, y, p->R, p->T, ld_y, 2)) g.whole |= 1;
+    if (p->T > 0 && c.slices == 1 && p->C % 64 == 0 && encode_chunks(&g.tm_t[1], p->type, a, p->C, p->T, ld_a, 4)) g.whole |= 2;
+    return launch(kernel, (int)c.units * c.split, c.split, D_THREADS, (size_t)c.stages * D_STAGE_BYTES + 1024, g, dev_status, stream);
+}
+
+extern "C" int sf_grouped_kernel(const sf_grouped *p, int product, int accumulate)
+{
+    if (product != SF_GROUPED_FORWARD && product != SF_GROUPED_DX && product != SF_GROUPED_DW) return SF_ERR_ARG;
+    const bool dw = product == SF_GROUPED_DW;
+    int rc = check_grouped(p, dw);
+    if (rc != SF_OK) return rc;
+    if (dw && accumulate && p->w_type != SF_TYPE_F32) return SF_ERR_ARG;
+    if (!dw && p->T == 0) return SF_GROUPED_NONE;
+    const int sms = sm_count();
+    if (sms <= 0) return SF_ERR_NO_DEVICE;
+    return dw ? choose_dw(p, accumulate != 0, sms).kernel : choose_product(p, product == SF_GROUPED_FORWARD, sms).kernel;
 }

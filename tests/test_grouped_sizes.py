@@ -45,3 +45,15 @@ def test_tiles_of_the_largest_counts_fit_32_bits(cnt, most):
     for x in (cnt + most - 1, cnt + tiles - 1, tile + 31, cnt + tile - 1, cnt + 63, n * tile, n * (tile // 32 + 4)):
         assert x < 2 ** 31
     assert tile <= most and n <= tiles
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="placeholder device pointers: host validation only")
+def test_the_kernels_query_refuses_what_the_calls_refuse(lib):  # noqa: F811
+    from tests.test_grouped_validation import REFUSED
+    for product in (0, 1, 2):
+        for case, kw, code in REFUSED:
+            assert lib.sf_grouped_kernel(ctypes.byref(_problem(**kw)), product, 0) == code, case
+        assert lib.sf_grouped_kernel(None, product, 0) == -1
+    assert lib.sf_grouped_kernel(ctypes.byref(_problem()), 3, 0) == -1
+    assert lib.sf_grouped_kernel(ctypes.byref(_problem()), 2, 1) == -1
+    assert lib.sf_grouped_kernel(ctypes.byref(_problem(T=0)), 0, 0) == b.SF_GROUPED_NONE
