@@ -323,12 +323,18 @@ class Helix:
 class Rewinder:
     """Binds a RewindPolicy (and optionally a Helix schedule) to device checkpoints of a list of
     matrices: `before_step(loss)` takes the previous step's loss, saves or restores through the
-    C ABI as the policy says, and returns the Action (skip means: do not apply this step)."""
+    C ABI as the policy says, and returns the Action (skip means: do not apply this step).
+    `dense` (a model.DensePlan), if given, is saved and restored with the matrices."""
+
+    dense = None
 
     def __init__(self, mats, policy: RewindPolicy | None = None, helix: Helix | None = None,
-                 device="cuda"):
+                 device="cuda", dense=None):
         from . import binding as sf
         self.sf = sf
+        self.dense = dense
+        if dense is not None:
+            dense.reserve()
         self.mats = list(mats)
         self.policy = policy or RewindPolicy()
         self.helix = helix
@@ -356,10 +362,14 @@ class Rewinder:
 
     def save(self, status=None, stream=None):
         self._call("sf_checkpoint_save", status, stream)
+        if self.dense is not None:
+            self.dense.save(0 if stream is None else stream)
         self.saved = True
 
     def restore(self, status=None, stream=None):
         self._call("sf_checkpoint_restore", status, stream)
+        if self.dense is not None:
+            self.dense.restore(0 if stream is None else stream)
 
     def before_step(self, loss: float, status=None, stream=None) -> Action:
         act = self.policy.observe(loss)

@@ -441,6 +441,35 @@ class DensePlan:
         self.with_norm = max_norm > 0.0 or inv_scale != 1.0
         self.norm = torch.zeros(2, dtype=torch.float32, device=device)
         self.ws = sf.grad_norm_workspace(self.tensors, device) if self.with_norm else None
+        self.copies = None
+
+    def state(self) -> list:
+        """What a step changes: weights, moments, scales, live copies and the step count."""
+        return [t for d in self.tensors.descs for k, t in enumerate(d.refs) if k != 1 and t is not None] + [self.steps]
+
+    def reserve(self):
+        """Buffers for one copy of the state, for save()."""
+        if self.copies is None:
+            self.copies = [torch.empty_like(t) for t in self.state()]
+
+    def save(self, stream=None):
+        """Copies the state aside (all of it: as much again as the tensors, their moments and live copies hold)."""
+        self.reserve()
+        self._copy(self.copies, self.state(), stream)
+
+    def restore(self, stream=None):
+        """Brings back the state of the last save()."""
+        if self.copies is None:
+            raise RuntimeError("nothing was saved")
+        self._copy(self.state(), self.copies, stream)
+
+    def _copy(self, into, of, stream):
+        if isinstance(stream, int):                      # a stream's address, as the rewinder passes it on
+            device = self.steps.device
+            stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+        with torch.cuda.stream(stream):
+            for a, b in zip(into, of):
+                a.copy_(b)
 
     def step(self, status=None, stream=None):
         if self.with_norm:
@@ -481,7 +510,8 @@ class Trainer:
     checkpoint, sets every pair's mix from the Helix schedule, and issues the step on `stream`,
     or skips it when the policy has just rewound. `pipes` are Pipeline objects over the same
     model (e.g. one per input bank); step k uses pipes[k % len(pipes)]. `dense` (a DensePlan) is
-    stepped behind the sparse step, on the same stream, and left out with it."""
+    stepped behind the sparse step, on the same stream, and left out, saved and restored with it
+    (a copy of its whole state each time)."""
 
     dense: DensePlan | None = None
 
@@ -493,7 +523,7 @@ class Trainer:
         self.dense = dense
         self.helix = helix if helix is not None else hx.Helix()
         self.rewinder = hx.Rewinder(model.all_mats, policy or hx.RewindPolicy(), self.helix,
-                                    device=device or model.device)
+                                    device=device or model.device, dense=dense)
         self.events = {}
 
     def step(self, k: int, prev_loss: float, tokens: torch.Tensor | None = None):
