@@ -430,18 +430,23 @@ class DensePlan:
     step: the argument array, the device step count and, with max_norm, the norm's workspace, built once.
 
     tensors: sf.Dense holders or sf.dense_tensor() descriptors; hp: their hyper-parameters; max_norm > 0 clips the
-    global norm of their gradients; inv_scale undoes a loss scale. A step whose gradients are not finite is
-    skipped on the device (max_norm or inv_scale given)."""
+    global norm of their gradients; inv_scale undoes a loss scale. Both may be changed from step to step. A step whose
+    gradients are not finite is skipped on the device (max_norm or inv_scale given)."""
 
     def __init__(self, tensors, hp: sf.AdamParams, max_norm: float = 0.0, inv_scale: float = 1.0):
+        if max_norm != max_norm or not inv_scale > 0.0:
+            raise ValueError(f"max_norm {max_norm}, inv_scale {inv_scale}: a number, and one above zero, expected")
         self.tensors = sf.DenseTensors(tensors)
         self.hp, self.max_norm, self.inv_scale = hp, max_norm, inv_scale
         device = hp.bc1.device
         self.steps = sf.step_words(device)
-        self.with_norm = max_norm > 0.0 or inv_scale != 1.0
         self.norm = torch.zeros(2, dtype=torch.float32, device=device)
-        self.ws = sf.grad_norm_workspace(self.tensors, device) if self.with_norm else None
+        self.ws = sf.grad_norm_workspace(self.tensors, device)
         self.copies = None
+
+    @property
+    def with_norm(self) -> bool:
+        return not self.max_norm <= 0.0 or self.inv_scale != 1.0
 
     def state(self) -> list:
         """What a step changes: weights, moments, scales, live copies and the step count."""
@@ -472,9 +477,10 @@ class DensePlan:
                 a.copy_(b)
 
     def step(self, status=None, stream=None):
-        if self.with_norm:
+        factor = self.norm if self.with_norm else None
+        if factor is not None:
             sf.sf_grad_norm(self.tensors, self.norm, self.ws, self.max_norm, self.inv_scale, status, stream)
-        sf.sf_adamw_step(self.tensors, self.hp, self.steps, self.norm if self.with_norm else None, status, stream)
+        sf.sf_adamw_step(self.tensors, self.hp, self.steps, factor, status, stream)
 
 
 class ExpertProjection:

@@ -115,3 +115,16 @@ def test_a_square_beyond_fp32_leaves_the_weight_finite(sf, size, at, state8, p_d
     tol = (4 * EPS32 + half_step(p_dt)) * np.abs(ref.p) + 40 * EPS32 * hp.lr
     assert np.all(np.abs(d.p.double().cpu().numpy() - ref.p) <= tol)
     assert int((~(d.v_scale if state8 else d.v).isfinite()).sum()) == 1
+
+
+def test_a_loss_scale_that_is_set_later(sf):
+    """A plan made without one takes it from the next step on; a power of two changes no bit."""
+    from masked_optimizer_step_b200.model import DensePlan
+    a = make(sf, 3000, torch.float32, torch.float32, sf.SF_TYPE_E4M3, True, 4)
+    b = sf.Dense(a.p.clone(), a.g * 1024.0, sf.SF_TYPE_E4M3, True)
+    plans = [DensePlan([d], sf.AdamParams(lr=1e-2)) for d in (a, b)]
+    plans[1].inv_scale = 2.0 ** -10
+    for _ in range(2):
+        for plan in plans:
+            plan.step()
+    assert torch.equal(a.p, b.p) and torch.equal(a.live, b.live) and torch.equal(a.m_scale, b.m_scale)
