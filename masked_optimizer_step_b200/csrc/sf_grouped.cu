@@ -68,6 +68,10 @@ constexpr size_t D_SMEM_BYTES = (size_t)D_MAX_STAGES * D_STAGE_BYTES + 1024;
 // truncation, so the error grows with the length (relative, normal values: 2.3e-7, 9.9e-7 and 9.1e-6 at 256, 1,024
 // and 8,192 tokens); 960 keep it below 1e-6 at any length.
 constexpr int W_CHUNK_STAGES = 960 / GK;
+// In 16 bits, whose rounding is 2^-9 or 2^-12 at its nearest: 8,192 tokens (9.1e-6). Only the pairs and four slices have a
+// place for their sums, in registers; calls that could make longer ones of one or two slices take those.
+constexpr int W16_CHUNK_STAGES = 8192 / GK;
+constexpr int W16_TOKENS = 65536;
 
 // Tokens to a tile, at most, that the pair kernel chooses from.
 constexpr int kCands = 15;
@@ -1414,7 +1418,13 @@ grouped_dw_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
             if (c < cols) prefetch_l2(w32 + r * g.ld_out + c);
         }
     const int nk = ((cnt + GK - 1) / GK + S * split - 1) / (S * split);      // steps of each slice
-    const int chunks = g.out_f32 ? quot_up(nk, W_CHUNK_STAGES) : 1, chunk = quot_up(nk, chunks);
+    const int chunks = g.out_f32 ? quot_up(nk, W_CHUNK_STAGES) : S == 4 ? quot_up(nk, W16_CHUNK_STAGES) : 1, chunk = quot_up(nk, chunks);
+    constexpr int HELD = S == 4 ? (SPLIT ? 1 : ROWS * (COLS / 4) / (32 * P_EPI_WARPS)) : 1;
+    float4 held[HELD];                          // S == 4, 16 bits: the chunks' sums of this thread's results
+    auto hold = [&](float4 s, int q, int ch) {  // true: the last chunk's are in
+        held[q] = ch == 0 ? s : make_float4(__fadd_rn(held[q].x, s.x), __fadd_rn(held[q].y, s.y), __fadd_rn(held[q].z, s.z), __fadd_rn(held[q].w, s.w));
+        return ch == chunks - 1;
+    };
     // slice j's tokens in its step i, those of the slice's end and of the expert's end left out
     const int step0 = rank * S * nk;            // of the slices before this CTA's
     auto tokens_of = [&](int j, int i) { return min(GK, cnt - (step0 + j * nk + i) * GK); };
@@ -1578,8 +1588,9 @@ grouped_dw_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                         *reinterpret_cast<uint4 *>(mine + c + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                 }
                 asm volatile("bar.sync 1, %0;" ::"r"(32 * P_EPI_WARPS) : "memory");
-                for (int i = tid - 64; i < ROWS * (COLS / 4); i += 32 * P_EPI_WARPS) {
-                    const int r = i / (COLS / 4), c = (i - r * (COLS / 4)) * 4;
+#pragma unroll (S == 4 ? 2 : 1)
+                for (int q = 0; q < ROWS * (COLS / 4) / (32 * P_EPI_WARPS); ++q) {
+                    const int i = tid - 64 + q * 32 * P_EPI_WARPS, r = i / (COLS / 4), c = (i - r * (COLS / 4)) * 4;
                     if (r >= rows || c >= cols) continue;
                     float4 s = *reinterpret_cast<const float4 *>(part_sums + r * PITCH + c);
 #pragma unroll
@@ -1588,7 +1599,8 @@ grouped_dw_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
                         s = make_float4(__fadd_rn(s.x, a.x), __fadd_rn(s.y, a.y), __fadd_rn(s.z, a.z), __fadd_rn(s.w, a.w));
                     }
                     if (SPLIT) *reinterpret_cast<float4 *>(part_sums + r * PITCH + c) = s;    // to be added to the other CTAs'
-                    else put_weights(g, w32, w16, r, c, s, add);
+                    else if (S != 4 || g.out_f32) put_weights(g, w32, w16, r, c, s, add);
+                    else if (hold(s, SPLIT ? 0 : q, ch)) put_weights(g, w32, w16, r, c, held[SPLIT ? 0 : q], false);
                 }
             }
         }
@@ -1601,23 +1613,18 @@ grouped_dw_small_kernel(const __grid_constant__ GArgs g, uint32_t *status)
             __syncwarp();
             cluster_sync();
             const uint32_t part_sums = smem_u32(smem);
-            auto add_up = [&](bool odd_ones) {
-                bool odd = false;
-                for (int i = rank * D_THREADS + tid; i < ROWS * (COLS / 4); i += split * D_THREADS) {
-                    const int r = i / (COLS / 4), c = (i - r * (COLS / 4)) * 4;
-                    if (r >= rows || c >= cols) continue;
-                    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int o = 0; o < split; ++o) {
-                        const uint32_t from = part_sums + (r * PITCH + c) * 4;
-                        const float2 a = ld_cluster_f32x2(from, o), b = ld_cluster_f32x2(from + 8, o);
-                        s = make_float4(__fadd_rn(s.x, a.x), __fadd_rn(s.y, a.y), __fadd_rn(s.z, b.x), __fadd_rn(s.w, b.y));
-                    }
-                    odd |= s.x != s.x;
-                    if ((s.x != s.x) == odd_ones) put_weights(g, w32, w16, r, c, s, add);
+            static_assert(!SPLIT || ROWS * (COLS / 4) <= 2 * D_THREADS, "a result to a thread");
+            const int i = rank * D_THREADS + tid, r = i / (COLS / 4), c = (i - r * (COLS / 4)) * 4;
+            if (i < ROWS * (COLS / 4) && r < rows && c < cols) {
+                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int o = 0; o < split; ++o) {
+                    const uint32_t from = part_sums + (r * PITCH + c) * 4;
+                    const float2 a = ld_cluster_f32x2(from, o), b = ld_cluster_f32x2(from + 8, o);
+                    s = make_float4(__fadd_rn(s.x, a.x), __fadd_rn(s.y, a.y), __fadd_rn(s.z, b.x), __fadd_rn(s.w, b.y));
                 }
-                return odd;
-            };
-            if (add_up(false) && !cluster_gave_up(&abort_flag, split)) add_up(true);
+                if (!g.out_f32 && hold(s, 0, ch)) s = held[0];
+                if ((g.out_f32 || ch == chunks - 1) && !(s.x != s.x && cluster_gave_up(&abort_flag, split))) put_weights(g, w32, w16, r, c, s, add);
+            }
             __syncwarp();
             cluster_sync();                     // no CTA goes on while others read its sums
         }
@@ -1880,17 +1887,18 @@ Choice choose_dw(const sf_grouped *p, bool accumulate, int sms)
     const int64_t busy = p->E < p->T ? p->E : p->T;      // experts with a token, at most
     // Pairs, unless they would be few, or one round of single CTAs does it all with short sums (8 experts of 1024 x 1024
     // over 128 tokens each: 11.1 us against 13.1; one of 2048 x 2048 over 4,096: 56 us against 30).
-    const bool one_round = busy * tiles(SM_ROWS, PN) <= 2 * sms && p->T <= (int64_t)512 * p->E;
-    if (busy * tiles(PM, PN) >= sms / 4 && !one_round) {
+    const bool long16 = p->w_type != SF_TYPE_F32 && p->T > W16_TOKENS;
+    const bool one_round = busy * tiles(SM_ROWS, PN) <= 2 * sms && p->T <= (int64_t)512 * p->E && !long16;
+    // Tokens in slices while the units still fit the device at once (one expert of 512 x 512 over 8,192 tokens: 102, 43 and
+    // 24 us with 1, 2 and 4 slices; where they do not fit, every slice more costs its share of the loads again).
+    int s = 1;
+    while (s < 4 && busy * tiles(SM_ROWS / (2 * s), PN / (2 * s)) <= 2 * sms && p->T > (int64_t)GK * s * p->E) s *= 2;
+    if ((busy * tiles(PM, PN) >= sms / 4 && !one_round) || (long16 && s < 4)) {
         const bool few = p->T < (accumulate ? kDwOldBelow : kDwFewBelow) * p->E;
         x.kernel = !few ? SF_GROUPED_PAIRS : accumulate ? SF_GROUPED_PAIRS_ADD : SF_GROUPED_PAIRS_FEW;
         x.units = p->E * tiles(PM, PN);
         return x;
     }
-    // Tokens in slices while the units still fit the device at once (one expert of 512 x 512 over 8,192 tokens: 102, 43 and
-    // 24 us with 1, 2 and 4 slices; where they do not fit, every slice more costs its share of the loads again).
-    int s = 1;
-    while (s < 4 && busy * tiles(SM_ROWS / (2 * s), PN / (2 * s)) <= 2 * sms && p->T > (int64_t)GK * s * p->E) s *= 2;
     x.slices = s;
     // Four slices in each CTA of a cluster while the CTAs fit one to an SM and keep more than four steps (alone against in
     // clusters: one expert of 128 x 128 over 65,536 tokens 151 / 31 us, of 64 x 512 over 8,192 tokens 22.3 / 9.5; with
