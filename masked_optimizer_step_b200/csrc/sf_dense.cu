@@ -618,12 +618,20 @@ grad_norm_kernel(const __grid_constant__ DenseBatch<N> b, int32_t *done, double 
 
 // ------------------------------------ host side ------------------------------------
 
+// Elements of a call: units, of a block of 256 to a warp at least, are numbered in 32 bits. Looked at before the first launch,
+// so that no call is refused half done.
+constexpr int64_t kMaxElements = (int64_t)1 << 40;
+static_assert(kMaxElements / (kWarps * kBlock) + SF_DENSE_PER_LAUNCH < 1 << 30, "units of a launch");
+
 int check_dense(const sf_dense *t, int n, bool step)
 {
     if (n < 0 || (n > 0 && !t)) return SF_ERR_ARG;
+    int64_t room = kMaxElements;
     for (int i = 0; i < n; ++i) {
         const sf_dense &a = t[i];
         if (a.n < 0) return SF_ERR_ARG;
+        if (a.n > room) return SF_ERR_UNSUPPORTED;
+        room -= a.n;
         if (a.g_type != SF_TYPE_F32 && a.g_type != SF_TYPE_BF16 && a.g_type != SF_TYPE_F16) return SF_ERR_ARG;
         if (a.n > 0 && !a.g) return SF_ERR_ARG;
         if (!aligned16(a.g)) return SF_ERR_ALIGN;
@@ -652,8 +660,7 @@ int unit_blocks(const sf_dense *t, int n, int sms, int most)
     return each >= most ? most : each >= 1 ? (int)each : 1;
 }
 
-// The next launch's tensors, from *at on: those with moments of the given type, or all (-1). Returns the units, or -1
-// when they pass 2^30.
+// The next launch's tensors, from *at on: those with moments of the given type, or all (-1). Returns the units.
 template <int N>
 int64_t fill(DenseBatch<N> &b, const sf_dense *t, int n, int *at, int per, int state)
 {
@@ -679,7 +686,6 @@ int64_t fill(DenseBatch<N> &b, const sf_dense *t, int n, int *at, int per, int s
         d.state_type = (uint8_t)a.state_type;
         d.pad = 0;
         units += (a.n + (int64_t)per * kWarps * kBlock - 1) / ((int64_t)per * kWarps * kBlock);
-        if (units > 1 << 30) return -1;
     }
     b.units = (int32_t)units;
     return units;
@@ -730,7 +736,6 @@ int launch_norm(const sf_dense *t, int n, int sms, const NormArgs &a)
     int64_t total = 0;
     for (int at = 0, first = 1; first || at < n; first = 0) {
         const int64_t units = fill(b, t, n, &at, per, -1);
-        if (units < 0) return SF_ERR_UNSUPPORTED;
         if (units > 0 || first) total += units < cap ? (units > 0 ? units : 1) : cap;
     }
     int32_t *done = static_cast<int32_t *>(a.ws);
@@ -757,7 +762,6 @@ int launch_step(const sf_dense *t, int n, int per, bool last, StepArgs a, uint32
     DenseBatch<N> b;
     for (int at = 0, li = 0; li < launches; ++li) {
         const int64_t units = fill(b, t, n, &at, per, state);
-        if (units < 0) return SF_ERR_UNSUPPORTED;
         a.last = last && li == launches - 1;
         // a CTA to a unit: dealt out as SMs come free (a 7B-shaped layer with 8-bit moments, when this was chosen: 518 us
         // against 588 with eight CTAs to an SM that took units in turn)
