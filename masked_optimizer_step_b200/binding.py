@@ -566,9 +566,16 @@ class DenseTensors:
         self.anchor = self.descs[0].refs[0] if self.n else None
         if self.n:
             _one_device(*[t for d in self.descs for t in d.refs])
-        written = [t.data_ptr() for d in self.descs for k, t in enumerate(d.refs) if k != 1 and t is not None and t.numel()]
-        if len(set(written)) != len(written):
-            raise ValueError("a tensor is in the list twice, or shares its weights or state with another")
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), k != 1)
+                       for d in self.descs for k, t in enumerate(d.refs) if t is not None and t.numel())
+        written_to = read_to = 0                         # ends of what the step writes and reads, from the lowest address up
+        for start, end, written in spans:
+            if start < written_to or (written and start < read_to):
+                raise ValueError("a tensor is in the list twice, or shares its weights or state with another, or with a gradient")
+            if written:
+                written_to = max(written_to, end)
+            else:
+                read_to = max(read_to, end)
 
 
 def step_words(device=None) -> torch.Tensor:
