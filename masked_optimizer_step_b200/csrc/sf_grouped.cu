@@ -68,10 +68,12 @@ constexpr size_t D_SMEM_BYTES = (size_t)D_MAX_STAGES * D_STAGE_BYTES + 1024;
 // truncation, so the error grows with the length (relative, normal values: 2.3e-7, 9.9e-7 and 9.1e-6 at 256, 1,024
 // and 8,192 tokens); 960 keep it below 1e-6 at any length.
 constexpr int W_CHUNK_STAGES = 960 / GK;
-// In 16 bits, whose rounding is 2^-9 or 2^-12 at its nearest: 8,192 tokens (9.1e-6). Only the pairs and four slices have a
-// place for their sums, in registers; calls that could make longer ones of one or two slices take those.
+// In 16 bits, which round by up to 2^-8 or 2^-11 (4.9e-4): 8,192 tokens in single CTAs. Sums of one sign drift by 5.5e-9 a token,
+// 4.5e-5 of those. Only the pairs and four slices have a place for their sums, in registers; calls that could make sums of more
+// than 32,768 tokens in one or two slices (1.8e-4) take those (1032 x 520 over 200,000 tokens, two slices against pairs: 905 us
+// and 5.6e-4 off on average, 1,195 us and 1.2e-5).
 constexpr int W16_CHUNK_STAGES = 8192 / GK;
-constexpr int W16_TOKENS = 65536;
+constexpr int W16_TOKENS = 32768;
 
 // Tokens to a tile, at most, that the pair kernel chooses from.
 constexpr int kCands = 15;
