@@ -944,7 +944,7 @@ __device__ __forceinline__ bool has_tail(const WUnit &x) { return (x.cnt & (G_UM
 
 // A pair sums 256 x 256 of W[e] over chunks of 960 tokens at most, in two accumulators in turn; the epilogue warps add the
 // chunks' sums in registers. What bounds it is the traffic between L2 and the SMs: 64 KB a stage and pair, 10.3 TB/s into
-// the SMs and 12.7 TB/s in all with the tensor cores 72% active (4 experts of 4096 x 4096 over 2,048 tokens each; the
+// the SMs and 12.9 TB/s in all with the tensor cores 72% active (4 experts of 4096 x 4096 over 2,048 tokens each; the
 // forward kernel's 512-column tiles take a quarter less and keep them 82% active). Wider tiles have no place for the sums:
 // 256 x 512 of fp32 are an SM pair's whole register files.
 // OLD: for gradients that are added to, over few tokens. What W holds comes into the output boxes by TMA while the MMAs
