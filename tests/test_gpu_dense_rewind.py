@@ -82,3 +82,19 @@ def test_the_steps_after_a_restore_are_those_after_the_save(sf):
         runs.append([bits(t) for t in plan.state()])
         plan.restore()
     assert all(torch.equal(a, b) for a, b in zip(*runs)) and plan.steps.tolist() == [2, 0]
+
+
+@pytest.mark.parametrize("state8", [False, True])
+def test_many_tensors_of_every_size_come_back(sf, state8):
+    from masked_optimizer_step_b200.model import DensePlan
+    lengths = [0, 1, 7, 255, 4096, 2 ** 18 - 1, 2 ** 18, 2 ** 18 + 5, 1_000_003] + [64] * 150
+    ds = [sf.Dense(normal((n,), torch.float32 if i % 2 else BF, i), normal((n,), BF, 500 + i), sf.SF_TYPE_E4M3 if state8 else sf.SF_TYPE_F32,
+                   live=i % 3 == 0) for i, n in enumerate(lengths)]
+    plan = DensePlan(ds, sf.AdamParams(lr=1e-2))
+    plan.step()
+    saved = [bits(t) for t in plan.state()]
+    plan.save()
+    plan.step()
+    assert not all(torch.equal(bits(t), b) for t, b in zip(plan.state(), saved))
+    plan.restore()
+    assert all(torch.equal(bits(t), b) for t, b in zip(plan.state(), saved))
